@@ -14,6 +14,10 @@ Calls (same names as the C ABI in include/moeq.h):
     combine_shared(y_perm, inv_perm, topk_w, y_shared) -> out
     forward(layer, x, logits, k, shared=None)   -> all of the above
     layer_forward(layer, x, logits, k)          -> topk_ids, topk_w, out (one C call)
+    block_norm, block_residual, combine_residual -- the norms, gate and residual
+        stream before and after a block (block.py)
+    quantize_i8, linear_i8, expert_ffn_i8, shared_ffn_i8, forward_i8 -- products
+        in 8-bit integers (I8Linear, I8Layer; block.py)
 Host packers: quantize_nvfp4, quantize_nvfp4_residual, pack_nvfp4_expert,
 pack_nvfp4r_expert, pack_vq_expert, pack_vq8_expert, pack_bf16_expert,
 record_bytes, record_table.  Test hook: dequant_q.
@@ -906,3 +910,12 @@ def forward(layer, x, logits, k, shared=None, overlap=False):
         r["y_shared"] = y_sh
         r["out"] = combine_shared(y_perm, inv_perm, w, y_sh)
     return r
+
+
+from . import block as _block_calls  # noqa: E402
+from .block import (DT_BF16, DT_F16, DT_F32, DT_I8, I8Layer, I8Linear, block_norm,  # noqa: E402,F401
+                    block_residual, codes_width, combine_residual, expert_ffn_i8,
+                    ffn_i8_workspace, forward_i8, linear_i8, linear_i8_workspace, quantize_i8,
+                    shared_ffn_i8)
+
+_PROTOS.update(_block_calls.PROTOS)

@@ -1,0 +1,167 @@
+// Device-side helpers of the calls that take rows of fp32, bf16 or fp16
+// (block norms, 8-bit quantisation): 8-element raw loads, their conversion to
+// fp32, rounding stores, and reductions over a workgroup.  gfx950 only.
+#pragma once
+
+#include "dev_common.h"
+
+namespace moeq {
+
+// Eight elements as loaded: 16 bytes of a 16-bit type (in a), or 32 of fp32.
+// The type is the same for a whole launch, so its branches are uniform; the
+// raw words stay unconverted until they are used, so that loads of several
+// operands are in flight together.
+struct Raw8 {
+    u32x4 a, b;
+};
+
+__device__ __forceinline__ Raw8 load_raw8(const void* p, int dt, int64_t i) {
+    Raw8 r;
+    if (dt == MOE_DT_F32) {
+        const u32x4* q = reinterpret_cast<const u32x4*>(static_cast<const float*>(p) + i);
+        r.a = q[0];
+        r.b = q[1];
+    } else {
+        r.a = *reinterpret_cast<const u32x4*>(static_cast<const uint16_t*>(p) + i);
+        r.b = u32x4{0u, 0u, 0u, 0u};
+    }
+    return r;
+}
+
+__device__ __forceinline__ void raw_to_f32(const Raw8& r, int dt, float (&v)[8]) {
+    if (dt == MOE_DT_F32) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            v[i] = __uint_as_float(r.a[i]);
+            v[4 + i] = __uint_as_float(r.b[i]);
+        }
+    } else if (dt == MOE_DT_BF16) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            v[2 * i] = __uint_as_float(r.a[i] << 16);
+            v[2 * i + 1] = __uint_as_float(r.a[i] & 0xffff0000u);
+        }
+    } else {
+        const f16x8 h = __builtin_bit_cast(f16x8, r.a);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v[i] = (float)h[i];
+    }
+}
+
+__device__ __forceinline__ float load_elem(const void* p, int dt, int64_t i) {
+    if (dt == MOE_DT_F32) return static_cast<const float*>(p)[i];
+    const uint16_t u = static_cast<const uint16_t*>(p)[i];
+    if (dt == MOE_DT_BF16) return __uint_as_float((uint32_t)u << 16);
+    return (float)__builtin_bit_cast(_Float16, u);
+}
+
+// V elements (8: one aligned vector, 1: a scalar) as fp32.
+template <int V>
+__device__ __forceinline__ void load_f32(const void* p, int dt, int64_t i, float (&v)[V]) {
+    if constexpr (V == 8) {
+        raw_to_f32(load_raw8(p, dt, i), dt, v);
+    } else {
+#pragma unroll
+        for (int e = 0; e < V; ++e) v[e] = load_elem(p, dt, i + e);
+    }
+}
+
+typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
+
+// fp32 -> bf16 bits of a pair, nearest even (NaN stays NaN).
+__device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
+    return __builtin_bit_cast(uint32_t, bf16x2{(__bf16)lo, (__bf16)hi});
+}
+__device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
+    return __builtin_bit_cast(uint32_t, f16x2{(_Float16)lo, (_Float16)hi});
+}
+
+// One rounding to the stored type, nearest even.
+template <int V>
+__device__ __forceinline__ void store_f32(void* p, int dt, int64_t i, const float (&v)[V]) {
+    if constexpr (V == 8) {
+        if (dt == MOE_DT_F32) {
+            f32x4* q = reinterpret_cast<f32x4*>(static_cast<float*>(p) + i);
+            q[0] = f32x4{v[0], v[1], v[2], v[3]};
+            q[1] = f32x4{v[4], v[5], v[6], v[7]};
+        } else {
+            u32x4 u;
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+                u[e] = dt == MOE_DT_BF16 ? pack_bf16(v[2 * e], v[2 * e + 1])
+                                         : pack_f16(v[2 * e], v[2 * e + 1]);
+            *reinterpret_cast<u32x4*>(static_cast<uint16_t*>(p) + i) = u;
+        }
+    } else {
+#pragma unroll
+        for (int e = 0; e < V; ++e) {
+            if (dt == MOE_DT_F32)
+                static_cast<float*>(p)[i + e] = v[e];
+            else
+                static_cast<uint16_t*>(p)[i + e] =
+                    (uint16_t)(dt == MOE_DT_BF16 ? pack_bf16(v[e], 0.f) : pack_f16(v[e], 0.f));
+        }
+    }
+}
+
+__device__ __forceinline__ float wave_sum(float v) {
+#pragma unroll
+    for (int off = 32; off >= 1; off >>= 1) v += __shfl_xor(v, off);
+    return v;
+}
+__device__ __forceinline__ uint32_t wave_max(uint32_t v) {
+#pragma unroll
+    for (int off = 32; off >= 1; off >>= 1) v = max(v, (uint32_t)__shfl_xor((int)v, off));
+    return v;
+}
+
+// Over the workgroup's nw waves, in wave order (the same bits in every
+// thread); red: one word per wave, not in use by another reduction.
+__device__ __forceinline__ float block_sum(float v, float* red, int nw) {
+    v = wave_sum(v);
+    if (nw == 1) return v;
+    if ((threadIdx.x & 63) == 0) red[threadIdx.x >> 6] = v;
+    __syncthreads();
+    float t = 0.f;
+    for (int i = 0; i < nw; ++i) t += red[i];
+    return t;
+}
+__device__ __forceinline__ uint32_t block_max(uint32_t v, uint32_t* red, int nw) {
+    v = wave_max(v);
+    if (nw == 1) return v;
+    if ((threadIdx.x & 63) == 0) red[threadIdx.x >> 6] = v;
+    __syncthreads();
+    uint32_t t = 0u;
+    for (int i = 0; i < nw; ++i) t = max(t, red[i]);
+    return t;
+}
+
+// The 8-bit code of a row: its scale and multiplier from the largest |v| of
+// the row (its bits: as integers they order like the magnitudes, and a NaN
+// or an infinity comes out above every finite value).
+//   finite a >= 127 * 2^-126:  scale a / 127, codes rint(v * (127 / a))
+//   smaller a (a row of zeros): scale 0, codes 0
+//   a row with an infinity or a NaN: scale NaN, codes 0
+struct RowCode {
+    float scale, mul;
+};
+__device__ __forceinline__ RowCode row_code(uint32_t amax_bits) {
+    const float a = __uint_as_float(amax_bits);
+    if (amax_bits >= 0x7f800000u) return RowCode{__uint_as_float(0x7fc00000u), 0.f};
+    if (a < 127.f * 0x1p-126f) return RowCode{0.f, 0.f};
+    return RowCode{a / 127.f, 127.f / a};
+}
+
+// v * mul rounded to the nearest integer, ties to even; |v * mul| <= 127
+// (1 + 2^-23) rounds to at most 127.  mul 0 gives 0 whatever v is.
+__device__ __forceinline__ int code_of(float v, float mul) {
+    return mul == 0.f ? 0 : (int)__builtin_rintf(v * mul);
+}
+__device__ __forceinline__ uint32_t pack_codes4(const float* v, float mul) {
+    uint32_t u = 0;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) u |= ((uint32_t)code_of(v[e], mul) & 0xffu) << (8 * e);
+    return u;
+}
+
+}  // namespace moeq

@@ -45,6 +45,12 @@ constexpr int kVq8TileK = 256;
 constexpr int kVq8TileBytesPerCode = 512;   // times m
 constexpr int kBf16TileK = 128;
 constexpr int kBf16TileBytes = 4096;
+// 8-bit integer matrices (moe_i8_linear, moe_i8_layer): row groups of 16 rows
+//   x tiles of 64 inputs = 1024 code bytes; lane L owns bytes [16L, 16L+16):
+//   row (L & 15), inputs kt*64 + (L >> 4)*16 + [0, 16), padded with zero codes.
+//   Gate/up matrices interleave row groups as above.
+constexpr int kI8TileK = 64;
+constexpr int kI8TileBytes = 1024;
 
 inline int64_t round_up(int64_t v, int64_t m) { return (v + m - 1) / m * m; }
 
@@ -65,6 +71,10 @@ inline int64_t vq8_codes_bytes(int32_t n, int32_t kin, int32_t m) {
 inline int64_t nv_record_bytes(int which, int32_t H, int32_t I) {
     return which == 0 ? round_up(nv_matrix_bytes(2 * I, H), 256)
                       : round_up(nv_matrix_bytes(H, I), 256);
+}
+inline int64_t i8_tiles_k(int32_t kin) { return round_up(kin, kI8TileK) / kI8TileK; }
+inline int64_t i8_matrix_bytes(int32_t n, int32_t kin) {
+    return round_up(n, 16) / 16 * i8_tiles_k(kin) * kI8TileBytes;
 }
 inline int64_t bf16_tiles_k(int32_t kin) { return round_up(kin, kBf16TileK) / kBf16TileK; }
 inline int64_t bf16_matrix_bytes(int32_t n, int32_t kin) {
@@ -199,6 +209,40 @@ int launch_layer_small_shared(const LayerView& L, int fmt, const LayerView& SL,
                               float* sh_part, float* out, void* stream);
 int launch_dequant(const LayerView& L, int fmt, int32_t rec_index, int32_t proj,
                    float* out, void* stream);
+// Block norms (vec8: H % 8 == 0 and every row of every operand 16-byte aligned).
+int launch_block(const moe_block& b, int64_t T, int32_t H, bool vec8, void* stream);
+// Rows to 8-bit codes with a scale each; codes padded with zeros to a multiple
+// of 64 (vec8: K % 8 == 0, x rows 16-byte and q rows 8-byte aligned).
+int launch_quantize_i8(const void* x, int dt, int64_t ldx, int64_t T, int32_t K, int8_t* q,
+                       int64_t ldq, float* scale, bool vec8, void* stream);
+// Row-major codes into 8-bit tiles, row group g to group g0 + g * step.
+int launch_pack_i8(const int8_t* codes, int64_t ld, int32_t N, int32_t K, int g0, int step,
+                   void* packed, void* stream);
+// One product pass of the 8-bit kernels, over the rows of q.
+//   pair = true:  groups interleave gate and up rows; h[row] = silu(g) * u
+//                 (fp32, rows ld_out apart), N = I channels;
+//   pair = false: out[row] = scale * wscale * sum (+ bias), N channels.
+// offsets == NULL: one matrix, output row r is q row r, rows r < T.
+// Otherwise output row r (in expert e's offsets range) reads q row
+// perm_src[r] / k, or q row r if perm_src is NULL.
+struct I8Pass {
+    const uint8_t* w;
+    int64_t w_stride;            // bytes per expert
+    const float* wscale;
+    int64_t wscale_stride;       // elements per expert
+    const float* bias;
+    const int8_t* q;
+    int64_t ldq;
+    const float* qscale;
+    const int32_t* offsets;
+    const int32_t* perm_src;
+    int64_t T;
+    int32_t E, k, N, K;
+    void* out;
+    int64_t ld_out;
+    int32_t out_dtype;
+};
+int launch_i8(const I8Pass& p, bool pair, void* stream);
 int launch_probe_read(const void* buf, size_t bytes, uint32_t* sink, int blocks, void* stream);
 
 }  // namespace moeq

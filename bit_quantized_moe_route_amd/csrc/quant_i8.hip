@@ -1,0 +1,151 @@
+// The 8-bit code of rows (a scale per row) and the device layout of 8-bit
+// weight matrices.
+//
+// Row t of x [T, K]:  a = max_k |x[t, k]|,  scale[t] = a / 127,
+// q[t, k] = rint(x[t, k] * (127 / a)).  One pass over x: a row stays in
+// registers (NCH chunks of V elements per thread) between its maximum and its
+// codes; rows past that (NCH = 0) are read a second time, from L2.
+#include <type_traits>
+
+#include "elem_dev.h"
+
+namespace moeq {
+
+namespace {
+
+struct QuantArgs {
+    const void* x;
+    int64_t ldx, ldq, T;
+    int8_t* q;
+    float* scale;
+    int dt, K, nw;   // nw: waves per row
+    int rows;        // rows per workgroup (one wave each when > 1)
+};
+
+template <int V>
+__device__ __forceinline__ void store_codes(int8_t* q, int h, const float (&v)[V], float mul) {
+    if constexpr (V == 8) {
+        const uint2 u = {pack_codes4(&v[0], mul), pack_codes4(&v[4], mul)};
+        *reinterpret_cast<uint2*>(q + h) = u;
+    } else {
+#pragma unroll
+        for (int e = 0; e < V; ++e) q[h + e] = (int8_t)code_of(v[e], mul);
+    }
+}
+
+template <int V, int NCH>
+__global__ __launch_bounds__(1024) void k_quantize(QuantArgs A) {
+    __shared__ uint32_t red[16];
+    const int tid = A.rows > 1 ? threadIdx.x & 63 : threadIdx.x;
+    const int nt = A.nw * 64;
+    const int64_t t = (int64_t)blockIdx.x * A.rows + (A.rows > 1 ? threadIdx.x >> 6 : 0);
+    if (t >= A.T) return;   // whole waves, and only where a row is one wave
+    int8_t* q = A.q + t * A.ldq;
+    uint32_t amax = 0u;
+    if constexpr (NCH > 0) {
+        float v[NCH][V];
+#pragma unroll
+        for (int c = 0; c < NCH; ++c) {
+            const int h = (c * nt + tid) * V;
+            if (h < A.K) {
+                load_f32<V>(A.x, A.dt, t * A.ldx + h, v[c]);
+            } else {
+#pragma unroll
+                for (int e = 0; e < V; ++e) v[c][e] = 0.f;
+            }
+        }
+#pragma unroll
+        for (int c = 0; c < NCH; ++c)
+#pragma unroll
+            for (int e = 0; e < V; ++e) amax = max(amax, __float_as_uint(v[c][e]) & 0x7fffffffu);
+        amax = block_max(amax, red, A.nw);
+        const RowCode rc = row_code(amax);
+        if (tid == 0) A.scale[t] = rc.scale;
+#pragma unroll
+        for (int c = 0; c < NCH; ++c) {
+            const int h = (c * nt + tid) * V;
+            if (h < A.K) store_codes<V>(q, h, v[c], rc.mul);
+        }
+    } else {
+        for (int h = tid * V; h < A.K; h += nt * V) {
+            float v[V];
+            load_f32<V>(A.x, A.dt, t * A.ldx + h, v);
+#pragma unroll
+            for (int e = 0; e < V; ++e) amax = max(amax, __float_as_uint(v[e]) & 0x7fffffffu);
+        }
+        amax = block_max(amax, red, A.nw);
+        const RowCode rc = row_code(amax);
+        if (tid == 0) A.scale[t] = rc.scale;
+        for (int h = tid * V; h < A.K; h += nt * V) {
+            float v[V];
+            load_f32<V>(A.x, A.dt, t * A.ldx + h, v);
+            store_codes<V>(q, h, v, rc.mul);
+        }
+    }
+    const int pad = (A.K + kI8TileK - 1) / kI8TileK * kI8TileK - A.K;
+    if (tid < pad) q[A.K + tid] = 0;
+}
+
+// Codes [N, K] (row-major, rows ld bytes apart) into 16-row x 64-input tiles
+// of 1024 bytes, lane L's 16 bytes = row L & 15, inputs (L >> 4) * 16 .. +16;
+// row group g of the matrix is group g0 + g * step of the destination.  A
+// wave writes one tile; rows and inputs past the matrix are zero codes.
+__global__ __launch_bounds__(256) void k_pack_i8(const int8_t* __restrict__ src, int64_t ld, int N,
+                                                 int K, int nkt, int64_t ntiles, int g0, int step,
+                                                 uint8_t* __restrict__ dst) {
+    const int64_t tile = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6);
+    if (tile >= ntiles) return;
+    const int lane = threadIdx.x & 63;
+    const int64_t g = tile / nkt;
+    const int kt = (int)(tile % nkt);
+    const int64_t n = g * 16 + (lane & 15);
+    const int k = kt * kI8TileK + (lane >> 4) * 16;
+    u32x4 u = {0u, 0u, 0u, 0u};
+    if (n < N) {
+#pragma unroll
+        for (int i = 0; i < 16; ++i)
+            if (k + i < K) u[i >> 2] |= (uint32_t)(uint8_t)src[n * ld + k + i] << (8 * (i & 3));
+    }
+    *reinterpret_cast<u32x4*>(dst + ((g0 + g * step) * nkt + kt) * kI8TileBytes + lane * 16) = u;
+}
+
+template <int V>
+void launch_q(QuantArgs A, hipStream_t s) {
+    const int nch = (A.K + V - 1) / V;
+    auto waves = [&](int per) { return (nch + 64 * per - 1) / (64 * per); };
+    auto go = [&](auto tag, int per) {
+        constexpr int NCH = decltype(tag)::value;
+        A.nw = per ? waves(per) : 16;
+        A.rows = 1;
+        k_quantize<V, NCH><<<(unsigned)A.T, A.nw * 64, 0, s>>>(A);
+    };
+    constexpr int C = V == 8 ? 1 : 8;
+    if (waves(C) <= 16) go(std::integral_constant<int, C>{}, C);
+    else if (waves(4 * C) <= 16) go(std::integral_constant<int, 4 * C>{}, 4 * C);
+    else go(std::integral_constant<int, 0>{}, 0);
+}
+
+}  // namespace
+
+int launch_quantize_i8(const void* x, int dt, int64_t ldx, int64_t T, int32_t K, int8_t* q,
+                       int64_t ldq, float* scale, bool vec8, void* stream) {
+    hipStream_t s = reinterpret_cast<hipStream_t>(stream);
+    QuantArgs A{x, ldx, ldq, T, q, scale, dt, K, 1, 1};
+    if (vec8) launch_q<8>(A, s);
+    else launch_q<1>(A, s);
+    MOEQ_CHECK_LAUNCH();
+    return MOE_OK;
+}
+
+int launch_pack_i8(const int8_t* codes, int64_t ld, int32_t N, int32_t K, int g0, int step,
+                   void* packed, void* stream) {
+    hipStream_t s = reinterpret_cast<hipStream_t>(stream);
+    const int64_t nkt = i8_tiles_k(K);
+    const int64_t ntiles = round_up(N, 16) / 16 * nkt;
+    k_pack_i8<<<(unsigned)((ntiles + 3) / 4), 256, 0, s>>>(codes, ld, N, K, (int)nkt, ntiles, g0,
+                                                           step, static_cast<uint8_t*>(packed));
+    MOEQ_CHECK_LAUNCH();
+    return MOE_OK;
+}
+
+}  // namespace moeq

@@ -536,6 +536,165 @@ int moe_layer_forward_shared(const moe_qlayer* layer, const moe_qlayer* shared,
                              int32_t* topk_ids, float* topk_w, float* out, void* workspace,
                              size_t workspace_bytes, void* stream);
 
+/* -------------------------------------------------- element types, 8-bit codes */
+
+/* Element types of the calls below (a tensor's rows may lie further apart
+ * than their width: ld* = elements between the starts of two rows). */
+#define MOE_DT_F32  1
+#define MOE_DT_BF16 2
+#define MOE_DT_F16  3
+#define MOE_DT_I8   4   /* 8-bit codes with an fp32 scale per row */
+
+/*
+ * moe_quantize_i8 -- the 8-bit code of every row of x:
+ *   a = max_k |x[t, k]|,  scale[t] = a / 127,
+ *   q[t, k] = rint(x[t, k] * (127 / a))    (fp32, ties to even; |q| <= 127)
+ *   A row whose a is below 127 * 2^-126 gets scale 0 and codes 0; a row that
+ *   holds an infinity or a NaN gets scale NaN and codes 0, so that every
+ *   product of that row is NaN and no other row is touched.
+ *   x      [device] [T, K] of x_dtype (F32, BF16, F16), rows ldx apart.
+ *   q      [device] int8 out, rows ldq apart: ldq a multiple of 16 and at least
+ *          K rounded up to 64, 16-byte aligned; the codes between K and that
+ *          are written as 0.
+ *   scale  [device] fp32 [T] out.
+ */
+int moe_quantize_i8(const void* x, int32_t x_dtype, int64_t ldx, int64_t T, int32_t K,
+                    int8_t* q, int64_t ldq, float* scale, void* stream);
+
+/* Bytes of a packed 8-bit [N, K] matrix (0 on bad sizes; K <= 131071, so that
+ * an int32 sum of K products cannot wrap). */
+size_t moe_i8_matrix_bytes(int32_t N, int32_t K);
+/* Bytes of one expert's 8-bit record: which = 0 gate/up, 1 down. */
+size_t moe_i8_record_bytes(int which, int32_t H, int32_t I);
+
+/*
+ * moe_pack_i8 -- lay int8 codes [device] [N, K] (rows ld apart, any values)
+ * out as the device tiles that moe_linear_i8 reads; packed [device] out,
+ * moe_i8_matrix_bytes(N, K) bytes, 16-byte aligned.  (Weights are quantised a
+ * row at a time like activations: moe_quantize_i8 with a row per output
+ * channel gives the codes and the channel scales.)
+ * moe_pack_i8_expert -- one expert's gate, up [I, H] and down [H, I] codes
+ * (row-major, contiguous) into its two records.
+ */
+int moe_pack_i8(const int8_t* codes, int64_t ld, int32_t N, int32_t K, void* packed,
+                void* stream);
+int moe_pack_i8_expert(const int8_t* gate, const int8_t* up, const int8_t* down, int32_t H,
+                       int32_t I, void* w13_rec, void* w2_rec, void* stream);
+
+/* A packed 8-bit matrix with a scale per output channel.  Host struct. */
+typedef struct moe_i8_linear {
+    int32_t N, K;
+    const void* w;          /* [device] from moe_pack_i8 */
+    const float* w_scale;   /* [device] fp32 [N] */
+    const float* bias;      /* [device] fp32 [N] or NULL */
+} moe_i8_linear;
+
+/*
+ * moe_linear_i8 -- out[t, n] = x_scale[t] * w_scale[n] * sum_k q[t, k] W[n, k]
+ * (+ bias[n]): the sum exact in int32, the rest in fp32, rounded once to
+ * out_dtype.
+ *   x          [device] codes (x_dtype MOE_DT_I8, rows as moe_quantize_i8
+ *              writes them, with x_scale [T]), or [T, K] of a float type,
+ *              which the call codes as moe_quantize_i8 does (x_scale NULL).
+ *   out        [device] [T, N] of out_dtype, rows ldo apart.
+ *   workspace  [device] >= moe_linear_i8_workspace_bytes(), 256-byte aligned;
+ *              unused (NULL allowed) when x is codes.
+ */
+size_t moe_linear_i8_workspace_bytes(const moe_i8_linear* linear, int64_t T);
+int moe_linear_i8(const moe_i8_linear* linear, const void* x, int32_t x_dtype, int64_t ldx,
+                  const float* x_scale, int64_t T, void* out, int32_t out_dtype, int64_t ldo,
+                  void* workspace, size_t workspace_bytes, void* stream);
+
+/* The experts of a layer in 8 bits.  Host struct; records of expert e at
+ * e * stride, from moe_pack_i8_expert. */
+typedef struct moe_i8_layer {
+    int32_t E, H, I, reserved;
+    const void* w13;  int64_t w13_stride;    /* bytes, multiples of 16 */
+    const void* w2;   int64_t w2_stride;
+    const float* w13_scale;                  /* [device] fp32 [E, 2I]: gate, then up */
+    const float* w2_scale;                   /* [device] fp32 [E, H] */
+} moe_i8_layer;
+
+/*
+ * moe_expert_ffn_i8 -- moe_expert_ffn_q over 8-bit weights and activations.
+ * For row i of the permuted order, e its expert and t = perm_src[i] / k:
+ *   g, u = products of token t's codes with gate and up of e, scaled
+ *   h = silu(g) * u               (fp32)
+ *   y_perm[i] = the product of h's 8-bit code (a scale per row, as
+ *               moe_quantize_i8) with down of e, scaled, rounded to y_dtype
+ *   x, x_dtype, ldx, x_scale as for moe_linear_i8 (K = H); perm_src, offsets
+ *   as for moe_expert_ffn_q; y_perm [device] [T*k, H] of y_dtype (fp32 for
+ *   moe_combine; moe_block_norm takes every type).
+ *   Any H and I from 1 to 131071.  workspace [device] >=
+ *   moe_expert_ffn_i8_workspace_bytes(), 256-byte aligned.
+ *
+ * moe_shared_ffn_i8 -- the same for a one-expert layer on every token:
+ * y_shared [T, H], workspace as above with k = 1.
+ */
+size_t moe_expert_ffn_i8_workspace_bytes(const moe_i8_layer* layer, int64_t T, int32_t k);
+int moe_expert_ffn_i8(const moe_i8_layer* layer, const void* x, int32_t x_dtype, int64_t ldx,
+                      const float* x_scale, const int32_t* perm_src, const int32_t* offsets,
+                      int64_t T, int32_t k, void* y_perm, int32_t y_dtype, void* workspace,
+                      size_t workspace_bytes, void* stream);
+int moe_shared_ffn_i8(const moe_i8_layer* shared, const void* x, int32_t x_dtype, int64_t ldx,
+                      const float* x_scale, int64_t T, void* y_shared, int32_t y_dtype,
+                      void* workspace, size_t workspace_bytes, void* stream);
+
+/* ------------------------------------------- norms before and after a block */
+
+#define MOE_BLOCK_MAX_H 32768
+
+/*
+ * moe_block_norm -- what lies between two blocks of a decoder layer, in one
+ * pass over each token's row: the gated sum of a routed layer or a block's
+ * output y, the norm after it, its gate, the scaled residual, the norm before
+ * the next block, and that block's input in 8 bits.  All in fp32:
+ *   b  = y[t]                                        (k == 0), or
+ *        sum_{j<k} topk_w[t, j] * y[inv_perm[t*k + j]]   (ascending j)
+ *        + shared_gate[t] * y_shared[t]              (k > 0)
+ *   p  = post_w ? N(b; post_w) : b
+ *   r' = r_scale * r + y_scale * gate * p
+ *   n  = pre_w ? N(r'; pre_w) : r'
+ *   N(v; w) = v / sqrt(mean(v^2) + eps) * (w_offset + w)
+ * n is taken from r' before r' is rounded to r_out.
+ *
+ *   y         [T, H] (k == 0), [T*k, H] (k > 0) or NULL (then r' = r_scale r:
+ *             the norm before a block alone).
+ *   gate      NULL (1), or gate[t * gate_ld_t + h * gate_ld_h]: per token
+ *             (gate_ld_h 0), per channel (gate_ld_t 0) or full.  gate_ld_h is
+ *             0 or 1.
+ *   r         [T, H] or NULL (0; needs y).  r_out (of r_dtype) may be r itself;
+ *             other outputs overlap no operand.
+ *   n_out     [T, H] of n_dtype, and / or q_out, q_scale: the 8-bit code of n,
+ *             as moe_quantize_i8 writes it.  Outputs that are NULL are not
+ *             written; at least one is given.
+ *   All pointers [device]; float operands are F32, BF16 or F16, post_w and
+ *   pre_w [H] of w_dtype.  Rows whose starts and strides are multiples of 16
+ *   bytes (and H of 8) take vector loads, others scalar ones.
+ *   Limits: 1 <= H <= MOE_BLOCK_MAX_H, 0 <= k <= MOE_MAX_K, eps >= 0.
+ *   The bits do not depend on T, and are the same run to run.
+ */
+typedef struct moe_block {
+    const void* y;            int64_t ld_y;
+    const int32_t* inv_perm;  const float* topk_w;
+    const void* y_shared;     int64_t ld_y_shared;
+    const float* shared_gate;
+    const void* post_w;
+    const void* gate;         int64_t gate_ld_t, gate_ld_h;
+    const void* r;            int64_t ld_r;
+    void* r_out;              int64_t ld_r_out;
+    const void* pre_w;
+    void* n_out;              int64_t ld_n;
+    int8_t* q_out;            int64_t ld_q;
+    float* q_scale;
+    int32_t k;
+    int32_t y_dtype, y_shared_dtype, r_dtype, w_dtype, gate_dtype, n_dtype;
+    float y_scale, r_scale, eps, w_offset;
+    int32_t reserved;
+} moe_block;
+
+int moe_block_norm(const moe_block* block, int64_t T, int32_t H, void* stream);
+
 /* ------------------------------------------------------- host-side packers */
 
 /*
