@@ -8,20 +8,16 @@
 // 16-byte load per lane) by up to 16 token rows (B: gathered 16-byte loads
 // from the caches).  The KS waves of a workgroup split the inputs and add
 // their int32 sums in LDS (integer sums: any order gives the same bits).
-#include "elem_dev.h"
+#include "i8_dev.h"
 
 namespace moeq {
 
 namespace {
 
-typedef int32_t i32x4 __attribute__((ext_vector_type(4)));
-
 __device__ __forceinline__ i32x4 mfma_i8(u32x4 a, u32x4 b, i32x4 acc) {
     return __builtin_amdgcn_mfma_i32_16x16x64_i8(__builtin_bit_cast(i32x4, a),
                                                  __builtin_bit_cast(i32x4, b), acc, 0, 0, 0);
 }
-
-__device__ __forceinline__ float silu_mul(float g, float u) { return g / (1.f + __expf(-g)) * u; }
 
 struct Rows {
     int e;          // expert, -1: none
@@ -55,12 +51,13 @@ __global__ __launch_bounds__(KS * 64) void k_i8(I8Pass A, int ngroups) {
     const int lane = threadIdx.x & 63, ks = threadIdx.x >> 6;
     const Rows rw = find_rows(A, blockIdx.y, lane);
     if (rw.e < 0) return;
-    const int nkt = (A.K + kI8TileK - 1) / kI8TileK;
+    const int nkt = (A.K + kI8TileK - 1) / kI8TileK;      // tiles with weights
+    const int64_t gbytes = i8_tiles_k(A.K) * kI8TileBytes;
     const int g0 = blockIdx.x * NG;
     const uint8_t* w[NG];
 #pragma unroll
     for (int g = 0; g < NG; ++g)
-        w[g] = A.w + rw.e * A.w_stride + (int64_t)min(g0 + g, ngroups - 1) * nkt * kI8TileBytes +
+        w[g] = A.w + rw.e * A.w_stride + min(g0 + g, ngroups - 1) * gbytes +
                lane * 16;
     const float* sw = A.wscale + rw.e * A.wscale_stride;
     const int k0 = (int)((int64_t)nkt * ks / KS), k1 = (int)((int64_t)nkt * (ks + 1) / KS);
@@ -120,6 +117,7 @@ __global__ __launch_bounds__(KS * 64) void k_i8(I8Pass A, int ngroups) {
 
 int launch_i8(const I8Pass& p, bool pair, void* stream) {
     hipStream_t s = reinterpret_cast<hipStream_t>(stream);
+    if ((p.offsets ? p.T * p.k / p.E : p.T) > 16) return launch_gemm_i8(p, pair, stream);
     const int ngroups = (int)(round_up(p.N, 16) / 16) * (pair ? 2 : 1);
     const int64_t slots = p.offsets ? (p.E < p.T * p.k ? p.E : p.T * p.k) : 1;
     const int64_t chunks = (p.T + 15) / 16;

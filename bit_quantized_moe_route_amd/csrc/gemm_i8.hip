@@ -1,0 +1,240 @@
+// Products in 8-bit integers for many rows: a grouped GEMM on
+// v_mfma_i32_32x32x32_i8 with the same results, bit for bit, as the
+// weight-streaming kernels (the sums are exact).
+//
+// A workgroup of 4 waves owns BM token rows of one expert (or of the whole
+// batch) x 256 record rows; each wave 64 of them: two 32-channel tiles, or 32
+// gate and the matching 32 up channels, so that SwiGLU is done in registers.
+//   * weights go straight from the packed tiles to registers (each byte is
+//     read by one wave), the next 128 inputs in flight while the current are
+//     multiplied;
+//   * the BM x 128 token codes are gathered through registers into LDS,
+//     double-buffered, 16-byte chunks XOR-swizzled by row.
+// Workgroups are dealt over the 8 XCDs by their channel tile, and inside one
+// XCD the token tiles of a channel tile follow each other, so that an expert
+// with several token tiles fetches its weights once and reads the rest in L2.
+#include "i8_dev.h"
+
+namespace moeq {
+
+namespace {
+
+typedef int32_t i32x16 __attribute__((ext_vector_type(16)));
+
+constexpr int kStageK = 128;
+
+__device__ __forceinline__ i32x16 mfma_i8_32(u32x4 a, u32x4 b, i32x16 acc) {
+    return __builtin_amdgcn_mfma_i32_32x32x32_i8(__builtin_bit_cast(i32x4, a),
+                                                 __builtin_bit_cast(i32x4, b), acc, 0, 0, 0);
+}
+
+struct GemmTile {
+    int e, n;            // expert (-1: none), channel tile
+    int64_t r0, m, m0;   // the expert's rows, the tile's first among them
+};
+
+// Workgroup blk's tile: XCD blk % 8 owns the channel tiles n = xcd mod 8.
+template <int BM>
+__device__ __forceinline__ GemmTile find_tile(const I8Pass& A, int blk, int nnt, int lane) {
+    GemmTile g{-1, 0, 0, 0, 0};
+    const int xcd = blk & 7, slot = blk >> 3;
+    const int nn = (nnt - xcd + 7) / 8;
+    if (nn <= 0) return g;
+    if (!A.offsets) {
+        const int nm = (int)((A.T + BM - 1) / BM);
+        if (slot / nm >= nn) return g;
+        return GemmTile{0, slot / nm * 8 + xcd, 0, A.T, (int64_t)(slot % nm) * BM};
+    }
+    const int want = slot / nn;
+    int before = 0;
+    for (int e0 = 0; e0 < A.E; e0 += 64) {
+        const int e = e0 + lane;
+        const int o0 = e < A.E ? A.offsets[e] : 0;
+        const int o1 = e < A.E ? A.offsets[e + 1] : 0;
+        const int nm = (o1 - o0 + BM - 1) / BM;
+        int incl = nm;
+#pragma unroll
+        for (int off = 1; off < 64; off <<= 1) {
+            const int v = __shfl_up(incl, off);
+            if (lane >= off) incl += v;
+        }
+        const int tot = __shfl(incl, 63);
+        if (want < before + tot) {
+            const int w = want - before;
+            const uint64_t mask = __ballot(w >= incl - nm && w < incl);
+            const int owner = __ffsll((unsigned long long)mask) - 1;
+            const int nmo = __shfl(nm, owner);
+            const int r = slot - (before + __shfl(incl, owner) - nmo) * nn;
+            g.e = e0 + owner;
+            g.r0 = __shfl(o0, owner);
+            g.m = __shfl(o1, owner) - g.r0;
+            g.n = r / nmo * 8 + xcd;
+            g.m0 = (int64_t)(r % nmo) * BM;
+            return g;
+        }
+        before += tot;
+    }
+    return g;
+}
+
+template <bool PAIR, int BM>
+__global__ __launch_bounds__(256, 2) void k_gemm_i8(I8Pass A, int ngroups, int nnt) {
+    constexpr int NT = BM / 32;                  // 32-row token tiles
+    __shared__ __attribute__((aligned(1024))) uint8_t tok[2][BM * kStageK];
+    __shared__ float qs[BM];
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    const GemmTile t = find_tile<BM>(A, blockIdx.x, nnt, lane);
+    if (t.e < 0) return;
+    const int Kp = (A.K + kI8TileK - 1) / kI8TileK * kI8TileK;
+    const int ns = (A.K + kStageK - 1) / kStageK;
+    const int left = (int)min((int64_t)BM, t.m - t.m0);   // rows of this tile
+    auto source = [&](int row) -> int64_t {
+        const int64_t r = t.r0 + t.m0 + min(row, left - 1);
+        return A.offsets && A.perm_src ? A.perm_src[r] / A.k : r;
+    };
+    if ((int)threadIdx.x < BM) qs[threadIdx.x] = A.qscale[source(threadIdx.x)];
+
+    // tokens: load i of a wave covers rows 8 (wave NT + i) .. + 8 of the tile
+    const int8_t* xp[NT];
+#pragma unroll
+    for (int i = 0; i < NT; ++i) xp[i] = A.q + source(8 * (wave * NT + i) + (lane >> 3)) * A.ldq;
+    u32x4 x[NT];
+    auto load_tokens = [&](int s) {
+        int k = s * kStageK + (lane & 7) * 16;
+        if (k >= Kp) k = 0;                      // the weights there are zero
+#pragma unroll
+        for (int i = 0; i < NT; ++i) x[i] = *reinterpret_cast<const u32x4*>(xp[i] + k);
+    };
+    // chunk c of row r lies at chunk c ^ (r & 7): reads of 8 rows hit all banks
+    const int xat = (lane >> 3) * kStageK + ((lane & 7) ^ (lane >> 3)) * 16;
+    auto put_tokens = [&](int buf) {
+#pragma unroll
+        for (int i = 0; i < NT; ++i)
+            *reinterpret_cast<u32x4*>(tok[buf] + (wave * NT + i) * 1024 + xat) = x[i];
+    };
+
+    // weights: 32-channel tile c of this wave, record groups of 16 rows
+    const int g0 = t.n * 16 + wave * 4;
+    const int half = (lane & 31) >> 4;
+    const uint8_t* wp[2];
+#pragma unroll
+    for (int c = 0; c < 2; ++c) {
+        const int g = min(g0 + (PAIR ? 2 * half + c : 2 * c + half), ngroups - 1);
+        wp[c] = A.w + t.e * A.w_stride + (int64_t)g * (2 * ns) * kI8TileBytes + (lane >> 5) * 256 +
+                (lane & 15) * 16;
+    }
+    i32x16 acc[NT][2];
+#pragma unroll
+    for (int i = 0; i < NT; ++i)
+#pragma unroll
+        for (int c = 0; c < 2; ++c)
+#pragma unroll
+            for (int v = 0; v < 16; ++v) acc[i][c][v] = 0;
+
+    // The weights of input step j are reloaded for the next stage as soon as
+    // they are multiplied: one set of registers, a whole stage of latency.
+    u32x4 w[2][4];
+    auto load_w = [&](int s, int j) {
+#pragma unroll
+        for (int c = 0; c < 2; ++c)
+            w[c][j] = *reinterpret_cast<const u32x4*>(wp[c] + (int64_t)s * 2048 + j * 512);
+    };
+#pragma unroll
+    for (int j = 0; j < 4; ++j) load_w(0, j);
+    load_tokens(0);
+    put_tokens(0);
+    for (int s = 0; s < ns; ++s) {
+        lds_barrier();
+        const int nx = min(s + 1, ns - 1);       // the last stage loads itself again
+        load_tokens(nx);
+        const uint8_t* base = tok[s & 1] + (lane & 31) * kStageK;
+        u32x4 a[2][NT];
+        auto read_a = [&](int j) {
+            const int at = ((2 * j + (lane >> 5)) ^ (lane & 7)) * 16;
+#pragma unroll
+            for (int i = 0; i < NT; ++i)
+                a[j & 1][i] = *reinterpret_cast<const u32x4*>(base + i * 32 * kStageK + at);
+        };
+        read_a(0);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            if (j < 3) read_a(j + 1);
+            if (j == 3) put_tokens((s + 1) & 1);
+#pragma unroll
+            for (int i = 0; i < NT; ++i)
+#pragma unroll
+                for (int c = 0; c < 2; ++c) acc[i][c] = mfma_i8_32(a[j & 1][i], w[c][j], acc[i][c]);
+            load_w(nx, j);
+            asm volatile("" ::: "memory");
+            __builtin_amdgcn_sched_barrier(0);
+        }
+    }
+
+    // lane: channel lane & 31 of each tile, rows 8 (v >> 2) + 4 (lane >> 5) + (v & 3)
+    const float* sw = A.wscale + t.e * A.wscale_stride;
+    const int col = lane & 31;
+    auto rows = [&](auto&& f) {
+#pragma unroll
+        for (int i = 0; i < NT; ++i)
+#pragma unroll
+            for (int v = 0; v < 16; ++v) {
+                const int row = 32 * i + 8 * (v >> 2) + 4 * (lane >> 5) + (v & 3);
+                if (row < left) f(i, v, qs[row], (t.r0 + t.m0 + row) * A.ld_out);
+            }
+    };
+    if constexpr (PAIR) {
+        const int ch = (t.n * 8 + wave * 2) * 16 + col;
+        if (ch >= A.N) return;
+        const float sg = sw[ch], su = sw[A.N + ch];
+        float* h = static_cast<float*>(A.out) + ch;
+        rows([&](int i, int v, float q, int64_t at) {
+            h[at] = silu_mul(q * sg * (float)acc[i][0][v], q * su * (float)acc[i][1][v]);
+        });
+    } else {
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+            const int ch = g0 * 16 + 32 * c + col;
+            if (ch >= A.N) continue;
+            const float s1 = sw[ch], bias = A.bias ? A.bias[ch] : 0.f;
+            auto value = [&](int i, int v, float q) {
+                const float y = q * s1 * (float)acc[i][c][v];
+                return A.bias ? y + bias : y;
+            };
+            if (A.out_dtype == MOE_DT_F32) {
+                float* o = static_cast<float*>(A.out) + ch;
+                rows([&](int i, int v, float q, int64_t at) { o[at] = value(i, v, q); });
+            } else if (A.out_dtype == MOE_DT_BF16) {
+                __bf16* o = static_cast<__bf16*>(A.out) + ch;
+                rows([&](int i, int v, float q, int64_t at) { o[at] = (__bf16)value(i, v, q); });
+            } else {
+                _Float16* o = static_cast<_Float16*>(A.out) + ch;
+                rows([&](int i, int v, float q, int64_t at) { o[at] = (_Float16)value(i, v, q); });
+            }
+        }
+    }
+}
+
+template <int BM>
+void launch(const I8Pass& p, bool pair, int ngroups, hipStream_t s) {
+    const int nnt = (ngroups + 15) / 16;
+    const int64_t rows = p.T * p.k;
+    const int64_t nm = p.offsets ? rows / BM + (p.E < rows ? p.E : rows) : (p.T + BM - 1) / BM;
+    const unsigned grid = (unsigned)(8 * nm * ((nnt + 7) / 8));
+    if (pair) k_gemm_i8<true, BM><<<grid, 256, 0, s>>>(p, ngroups, nnt);
+    else k_gemm_i8<false, BM><<<grid, 256, 0, s>>>(p, ngroups, nnt);
+}
+
+}  // namespace
+
+int launch_gemm_i8(const I8Pass& p, bool pair, void* stream) {
+    hipStream_t s = reinterpret_cast<hipStream_t>(stream);
+    const int ngroups = (int)(round_up(p.N, 16) / 16) * (pair ? 2 : 1);
+    const int64_t mean = p.offsets ? p.T * p.k / p.E : p.T;
+    if (mean > 64) launch<128>(p, pair, ngroups, s);
+    else if (mean > 32) launch<64>(p, pair, ngroups, s);
+    else launch<32>(p, pair, ngroups, s);
+    MOEQ_CHECK_LAUNCH();
+    return MOE_OK;
+}
+
+}  // namespace moeq

@@ -47,8 +47,8 @@ constexpr int kBf16TileK = 128;
 constexpr int kBf16TileBytes = 4096;
 // 8-bit integer matrices (moe_i8_linear, moe_i8_layer): row groups of 16 rows
 //   x tiles of 64 inputs = 1024 code bytes; lane L owns bytes [16L, 16L+16):
-//   row (L & 15), inputs kt*64 + (L >> 4)*16 + [0, 16), padded with zero codes.
-//   Gate/up matrices interleave row groups as above.
+//   row (L & 15), inputs kt*64 + (L >> 4)*16 + [0, 16), padded with zero codes
+//   to an even number of tiles.  Gate/up matrices interleave row groups as above.
 constexpr int kI8TileK = 64;
 constexpr int kI8TileBytes = 1024;
 
@@ -72,7 +72,9 @@ inline int64_t nv_record_bytes(int which, int32_t H, int32_t I) {
     return which == 0 ? round_up(nv_matrix_bytes(2 * I, H), 256)
                       : round_up(nv_matrix_bytes(H, I), 256);
 }
-inline int64_t i8_tiles_k(int32_t kin) { return round_up(kin, kI8TileK) / kI8TileK; }
+constexpr int64_t i8_tiles_k(int32_t kin) {
+    return ((int64_t)kin + 2 * kI8TileK - 1) / (2 * kI8TileK) * 2;
+}
 inline int64_t i8_matrix_bytes(int32_t n, int32_t kin) {
     return round_up(n, 16) / 16 * i8_tiles_k(kin) * kI8TileBytes;
 }
@@ -243,6 +245,7 @@ struct I8Pass {
     int32_t out_dtype;
 };
 int launch_i8(const I8Pass& p, bool pair, void* stream);
+int launch_gemm_i8(const I8Pass& p, bool pair, void* stream);
 int launch_probe_read(const void* buf, size_t bytes, uint32_t* sink, int blocks, void* stream);
 
 }  // namespace moeq

@@ -169,8 +169,8 @@ def test_quantize_refusals(args, status):
 
 def test_matrix_sizes_and_pack_refusals():
     L = moeq.lib()
-    assert L.moe_i8_matrix_bytes(16, 64) == 1024 and L.moe_i8_matrix_bytes(17, 65) == 4096
-    assert L.moe_i8_record_bytes(0, 65, 17) == 2 * 4096 and L.moe_i8_record_bytes(1, 17, 65) == 4096
+    assert L.moe_i8_matrix_bytes(16, 64) == 2048 and L.moe_i8_matrix_bytes(17, 129) == 8192
+    assert L.moe_i8_record_bytes(0, 65, 17) == 2 * 4096 and L.moe_i8_record_bytes(1, 17, 129) == 8192
     for n, k in ((0, 64), (16, 0), (16, 131072), ((1 << 24) + 1, 64)):
         assert L.moe_i8_matrix_bytes(n, k) == 0
     assert L.moe_i8_record_bytes(2, 64, 64) == 0 and L.moe_i8_record_bytes(0, 64, 131072) == 0
@@ -216,7 +216,7 @@ def test_linear_refusals(desc, args, status):
 
 
 def lay(**kw):
-    d = dict(E=4, H=64, I=32, w13=P, w13_stride=4096, w2=P, w2_stride=4096, w13_scale=P,
+    d = dict(E=4, H=64, I=32, w13=P, w13_stride=8192, w2=P, w2_stride=8192, w13_scale=P,
              w2_scale=P)
     d.update(kw)
     return ctypes.byref(mb.I8LayerC(**d))
@@ -224,7 +224,7 @@ def lay(**kw):
 
 @pytest.mark.parametrize("desc", [dict(E=0), dict(E=1025), dict(H=0), dict(I=0), dict(w13=None),
                                   dict(w2_scale=None), dict(w13=P + 4), dict(w2_stride=4104),
-                                  dict(w13_stride=2048), dict(w2_stride=1024)])
+                                  dict(w13_stride=4096), dict(w2_stride=4096)])
 def test_layer_refusals(desc):
     refused("moe_expert_ffn_i8", lay(**desc), P, 2, 64, None, P, P, 1, 1, P, 2, P, 1 << 20, None)
     if "E" not in desc:
