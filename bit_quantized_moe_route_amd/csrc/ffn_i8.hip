@@ -102,8 +102,8 @@ __global__ __launch_bounds__(KS * 64) void k_i8(I8Pass A, int ngroups) {
 #pragma unroll
                     for (int i = 0; i < 4; ++i)
                         if (g0 + g < ngroups && ch + i < A.N) {
-                            float y[1] = {sq * sw[ch + i] * (float)acc[g][i]};
-                            if (A.bias) y[0] += A.bias[ch + i];
+                            const float b = A.bias ? A.bias[ch + i] : 0.f;
+                            const float y[1] = {sq * sw[ch + i] * (float)acc[g][i] + b};
                             store_f32<1>(A.out, A.out_dtype, row * A.ld_out + ch + i, y);
                         }
                 }
@@ -120,9 +120,9 @@ int launch_i8(const I8Pass& p, bool pair, void* stream) {
     if ((p.offsets ? p.T * p.k / p.E : p.T) > 16) return launch_gemm_i8(p, pair, stream);
     const int ngroups = (int)(round_up(p.N, 16) / 16) * (pair ? 2 : 1);
     const int64_t slots = p.offsets ? (p.E < p.T * p.k ? p.E : p.T * p.k) : 1;
-    const int64_t chunks = (p.T + 15) / 16;
-    const dim3 grid((unsigned)((ngroups + 1) / 2), (unsigned)slots,
-                    (unsigned)(chunks < 1024 ? chunks : 1024));
+    // a workgroup takes its matrix's 16-row chunks in turn
+    const int64_t rows = p.offsets ? p.T * p.k / p.E : p.T;
+    const dim3 grid((unsigned)((ngroups + 1) / 2), (unsigned)slots, (unsigned)(rows / 16 + 1));
     if (pair) k_i8<true, 2, 4><<<grid, 256, 0, s>>>(p, ngroups);
     else k_i8<false, 2, 4><<<grid, 256, 0, s>>>(p, ngroups);
     MOEQ_CHECK_LAUNCH();

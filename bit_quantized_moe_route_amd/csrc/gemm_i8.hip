@@ -13,6 +13,8 @@
 // Workgroups are dealt over the 8 XCDs by their channel tile, and inside one
 // XCD the token tiles of a channel tile follow each other, so that an expert
 // with several token tiles fetches its weights once and reads the rest in L2.
+#include <type_traits>
+
 #include "i8_dev.h"
 
 namespace moeq {
@@ -78,7 +80,7 @@ __device__ __forceinline__ GemmTile find_tile(const I8Pass& A, int blk, int nnt,
 }
 
 template <bool PAIR, int BM>
-__global__ __launch_bounds__(256, 2) void k_gemm_i8(I8Pass A, int ngroups, int nnt) {
+__global__ __launch_bounds__(256, 2) void k_gemm_i8(I8Pass A, int ngroups, int nnt, bool pairs) {
     constexpr int NT = BM / 32;                  // 32-row token tiles
     __shared__ __attribute__((aligned(1024))) uint8_t tok[2][BM * kStageK];
     __shared__ float qs[BM];
@@ -88,129 +90,158 @@ __global__ __launch_bounds__(256, 2) void k_gemm_i8(I8Pass A, int ngroups, int n
     const int Kp = (A.K + kI8TileK - 1) / kI8TileK * kI8TileK;
     const int ns = (A.K + kStageK - 1) / kStageK;
     const int left = (int)min((int64_t)BM, t.m - t.m0);   // rows of this tile
+    const int64_t first = t.r0 + t.m0;
     auto source = [&](int row) -> int64_t {
-        const int64_t r = t.r0 + t.m0 + min(row, left - 1);
+        const int64_t r = first + min(row, left - 1);
         return A.offsets && A.perm_src ? A.perm_src[r] / A.k : r;
     };
     if ((int)threadIdx.x < BM) qs[threadIdx.x] = A.qscale[source(threadIdx.x)];
 
-    // tokens: load i of a wave covers rows 8 (wave NT + i) .. + 8 of the tile
+    // tokens: load i of a wave covers rows 32 i + 8 wave .. + 8 of the tile
     const int8_t* xp[NT];
 #pragma unroll
-    for (int i = 0; i < NT; ++i) xp[i] = A.q + source(8 * (wave * NT + i) + (lane >> 3)) * A.ldq;
-    u32x4 x[NT];
-    auto load_tokens = [&](int s) {
-        int k = s * kStageK + (lane & 7) * 16;
-        if (k >= Kp) k = 0;                      // the weights there are zero
-#pragma unroll
-        for (int i = 0; i < NT; ++i) x[i] = *reinterpret_cast<const u32x4*>(xp[i] + k);
-    };
+    for (int i = 0; i < NT; ++i) xp[i] = A.q + source(32 * i + 8 * wave + (lane >> 3)) * A.ldq;
     // chunk c of row r lies at chunk c ^ (r & 7): reads of 8 rows hit all banks
-    const int xat = (lane >> 3) * kStageK + ((lane & 7) ^ (lane >> 3)) * 16;
-    auto put_tokens = [&](int buf) {
-#pragma unroll
-        for (int i = 0; i < NT; ++i)
-            *reinterpret_cast<u32x4*>(tok[buf] + (wave * NT + i) * 1024 + xat) = x[i];
-    };
+    const int xat = wave * 8 * kStageK + (lane >> 3) * kStageK + ((lane & 7) ^ (lane >> 3)) * 16;
 
-    // weights: 32-channel tile c of this wave, record groups of 16 rows
+    // weights: tiles c = 0, 1 of this wave's 64 record rows; a lane's column is
+    // channel lane & 31 of the gate (0) and up (1) rows, or, one matrix alone,
+    // record row 2 (lane & 31) + c, so that a lane has two neighbours to store.
     const int g0 = t.n * 16 + wave * 4;
-    const int half = (lane & 31) >> 4;
+    const int col = lane & 31;
     const uint8_t* wp[2];
 #pragma unroll
     for (int c = 0; c < 2; ++c) {
-        const int g = min(g0 + (PAIR ? 2 * half + c : 2 * c + half), ngroups - 1);
+        const int r = PAIR ? col : 2 * col + c;
+        const int g = min(g0 + (PAIR ? 2 * (r >> 4) + c : r >> 4), ngroups - 1);
         wp[c] = A.w + t.e * A.w_stride + (int64_t)g * (2 * ns) * kI8TileBytes + (lane >> 5) * 256 +
-                (lane & 15) * 16;
+                (r & 15) * 16;
     }
-    i32x16 acc[NT][2];
-#pragma unroll
-    for (int i = 0; i < NT; ++i)
-#pragma unroll
-        for (int c = 0; c < 2; ++c)
-#pragma unroll
-            for (int v = 0; v < 16; ++v) acc[i][c][v] = 0;
-
-    // The weights of input step j are reloaded for the next stage as soon as
-    // they are multiplied: one set of registers, a whole stage of latency.
-    u32x4 w[2][4];
-    auto load_w = [&](int s, int j) {
-#pragma unroll
-        for (int c = 0; c < 2; ++c)
-            w[c][j] = *reinterpret_cast<const u32x4*>(wp[c] + (int64_t)s * 2048 + j * 512);
-    };
-#pragma unroll
-    for (int j = 0; j < 4; ++j) load_w(0, j);
-    load_tokens(0);
-    put_tokens(0);
-    for (int s = 0; s < ns; ++s) {
-        lds_barrier();
-        const int nx = min(s + 1, ns - 1);       // the last stage loads itself again
-        load_tokens(nx);
-        const uint8_t* base = tok[s & 1] + (lane & 31) * kStageK;
-        u32x4 a[2][NT];
-        auto read_a = [&](int j) {
-            const int at = ((2 * j + (lane >> 5)) ^ (lane & 7)) * 16;
-#pragma unroll
-            for (int i = 0; i < NT; ++i)
-                a[j & 1][i] = *reinterpret_cast<const u32x4*>(base + i * 32 * kStageK + at);
-        };
-        read_a(0);
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            if (j < 3) read_a(j + 1);
-            if (j == 3) put_tokens((s + 1) & 1);
-#pragma unroll
-            for (int i = 0; i < NT; ++i)
-#pragma unroll
-                for (int c = 0; c < 2; ++c) acc[i][c] = mfma_i8_32(a[j & 1][i], w[c][j], acc[i][c]);
-            load_w(nx, j);
-            asm volatile("" ::: "memory");
-            __builtin_amdgcn_sched_barrier(0);
-        }
-    }
-
-    // lane: channel lane & 31 of each tile, rows 8 (v >> 2) + 4 (lane >> 5) + (v & 3)
     const float* sw = A.wscale + t.e * A.wscale_stride;
-    const int col = lane & 31;
-    auto rows = [&](auto&& f) {
+
+    // NB of the tile's 32-row token tiles hold rows
+    auto run = [&](auto nb) {
+        constexpr int NB = decltype(nb)::value;
+        u32x4 x[NB], w[2][4];
+        auto load_tokens = [&](int s) {
+            int k = s * kStageK + (lane & 7) * 16;
+            if (k >= Kp) k = 0;                  // the weights there are zero
 #pragma unroll
-        for (int i = 0; i < NT; ++i)
+            for (int i = 0; i < NB; ++i) x[i] = *reinterpret_cast<const u32x4*>(xp[i] + k);
+        };
+        auto put_tokens = [&](int buf) {
 #pragma unroll
-            for (int v = 0; v < 16; ++v) {
-                const int row = 32 * i + 8 * (v >> 2) + 4 * (lane >> 5) + (v & 3);
-                if (row < left) f(i, v, qs[row], (t.r0 + t.m0 + row) * A.ld_out);
-            }
-    };
-    if constexpr (PAIR) {
-        const int ch = (t.n * 8 + wave * 2) * 16 + col;
-        if (ch >= A.N) return;
-        const float sg = sw[ch], su = sw[A.N + ch];
-        float* h = static_cast<float*>(A.out) + ch;
-        rows([&](int i, int v, float q, int64_t at) {
-            h[at] = silu_mul(q * sg * (float)acc[i][0][v], q * su * (float)acc[i][1][v]);
-        });
-    } else {
+            for (int i = 0; i < NB; ++i)
+                *reinterpret_cast<u32x4*>(tok[buf] + i * 32 * kStageK + xat) = x[i];
+        };
+        // The weights of input step j are reloaded for the next stage as soon as
+        // they are multiplied: one set of registers, a whole stage of latency.
+        auto load_w = [&](int s, int j) {
 #pragma unroll
-        for (int c = 0; c < 2; ++c) {
-            const int ch = g0 * 16 + 32 * c + col;
-            if (ch >= A.N) continue;
-            const float s1 = sw[ch], bias = A.bias ? A.bias[ch] : 0.f;
-            auto value = [&](int i, int v, float q) {
-                const float y = q * s1 * (float)acc[i][c][v];
-                return A.bias ? y + bias : y;
+            for (int c = 0; c < 2; ++c)
+                w[c][j] = *reinterpret_cast<const u32x4*>(wp[c] + (int64_t)s * 2048 + j * 512);
+        };
+        i32x16 acc[NB][2];
+#pragma unroll
+        for (int i = 0; i < NB; ++i)
+#pragma unroll
+            for (int c = 0; c < 2; ++c)
+#pragma unroll
+                for (int v = 0; v < 16; ++v) acc[i][c][v] = 0;
+        load_tokens(0);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) load_w(0, j);
+        put_tokens(0);
+        for (int s = 0; s < ns; ++s) {
+            lds_barrier();
+            const int nx = min(s + 1, ns - 1);   // the last stage loads itself again
+            load_tokens(nx);
+            const uint8_t* base = tok[s & 1] + col * kStageK;
+            u32x4 a[2][NB];
+            auto read_a = [&](int j) {
+                const int at = ((2 * j + (lane >> 5)) ^ (lane & 7)) * 16;
+#pragma unroll
+                for (int i = 0; i < NB; ++i)
+                    a[j & 1][i] = *reinterpret_cast<const u32x4*>(base + i * 32 * kStageK + at);
             };
-            if (A.out_dtype == MOE_DT_F32) {
-                float* o = static_cast<float*>(A.out) + ch;
-                rows([&](int i, int v, float q, int64_t at) { o[at] = value(i, v, q); });
-            } else if (A.out_dtype == MOE_DT_BF16) {
-                __bf16* o = static_cast<__bf16*>(A.out) + ch;
-                rows([&](int i, int v, float q, int64_t at) { o[at] = (__bf16)value(i, v, q); });
-            } else {
-                _Float16* o = static_cast<_Float16*>(A.out) + ch;
-                rows([&](int i, int v, float q, int64_t at) { o[at] = (_Float16)value(i, v, q); });
+            read_a(0);
+            keep_order();
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                if (j < 3) read_a(j + 1);
+                else put_tokens((s + 1) & 1);
+#pragma unroll
+                for (int i = 0; i < NB; ++i)
+#pragma unroll
+                    for (int c = 0; c < 2; ++c)
+                        acc[i][c] = mfma_i8_32(a[j & 1][i], w[c][j], acc[i][c]);
+                load_w(nx, j);
+                // one LDS access of the next step between every two products
+#pragma unroll
+                for (int i = 0; i < NB; ++i) {
+                    if (j < 3) __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
+                    else __builtin_amdgcn_sched_group_barrier(0x200, 1, 0);
+                    __builtin_amdgcn_sched_group_barrier(0x008, 2, 0);
+                }
+                __builtin_amdgcn_sched_group_barrier(0x020, 2, 0);
+                keep_order();
             }
         }
+
+        // lane: rows 32 i + 8 (v >> 2) + 4 (lane >> 5) + (v & 3) of its column
+        auto rows = [&](auto&& f) {
+#pragma unroll
+            for (int i = 0; i < NB; ++i)
+#pragma unroll
+                for (int v = 0; v < 16; ++v) {
+                    const int row = 32 * i + 8 * (v >> 2) + 4 * (lane >> 5) + (v & 3);
+                    if (row < left) f(qs[row], acc[i][0][v], acc[i][1][v], (first + row) * A.ld_out);
+                }
+        };
+        if constexpr (PAIR) {
+            const int ch = g0 * 8 + col;
+            if (ch >= A.N) return;
+            const float sg = sw[ch], su = sw[A.N + ch];
+            float* h = static_cast<float*>(A.out) + ch;
+            rows([&](float q, int g, int u, int64_t at) {
+                h[at] = silu_mul(q * sg * (float)g, q * su * (float)u);
+            });
+        } else {
+            const int ch = g0 * 16 + 2 * col;
+            if (ch >= A.N) return;
+            const bool two = ch + 1 < A.N;
+            const float s0 = sw[ch], s1 = two ? sw[ch + 1] : 0.f;
+            const float b0 = A.bias ? A.bias[ch] : 0.f, b1 = A.bias && two ? A.bias[ch + 1] : 0.f;
+            auto store = [&](auto zero) {
+                using T = decltype(zero);
+                typedef T T2 __attribute__((ext_vector_type(2)));
+                T* o = static_cast<T*>(A.out) + ch;
+                rows([&](float q, int a0, int a1, int64_t at) {
+                    const T y0 = (T)(q * s0 * (float)a0 + b0), y1 = (T)(q * s1 * (float)a1 + b1);
+                    if (pairs) {
+                        *reinterpret_cast<T2*>(o + at) = T2{y0, y1};
+                    } else {
+                        o[at] = y0;
+                        if (two) o[at + 1] = y1;
+                    }
+                });
+            };
+            if (A.out_dtype == MOE_DT_F32) store(0.f);
+            else if (A.out_dtype == MOE_DT_BF16) store((__bf16)0.f);
+            else store((_Float16)0.f);
+        }
+    };
+    const int nb = (left + 31) / 32;
+    if constexpr (NT == 1) {
+        run(std::integral_constant<int, 1>{});
+    } else if constexpr (NT == 2) {
+        if (nb == 1) run(std::integral_constant<int, 1>{});
+        else run(std::integral_constant<int, 2>{});
+    } else {
+        if (nb == 1) run(std::integral_constant<int, 1>{});
+        else if (nb == 2) run(std::integral_constant<int, 2>{});
+        else if (nb == 3) run(std::integral_constant<int, 3>{});
+        else run(std::integral_constant<int, 4>{});
     }
 }
 
@@ -220,8 +251,12 @@ void launch(const I8Pass& p, bool pair, int ngroups, hipStream_t s) {
     const int64_t rows = p.T * p.k;
     const int64_t nm = p.offsets ? rows / BM + (p.E < rows ? p.E : rows) : (p.T + BM - 1) / BM;
     const unsigned grid = (unsigned)(8 * nm * ((nnt + 7) / 8));
-    if (pair) k_gemm_i8<true, BM><<<grid, 256, 0, s>>>(p, ngroups, nnt);
-    else k_gemm_i8<false, BM><<<grid, 256, 0, s>>>(p, ngroups, nnt);
+    // two neighbouring channels in one store
+    const uintptr_t two = p.out_dtype == MOE_DT_F32 ? 8 : 4;
+    const bool pairs = p.N % 2 == 0 && p.ld_out % 2 == 0 &&
+                       reinterpret_cast<uintptr_t>(p.out) % two == 0;
+    if (pair) k_gemm_i8<true, BM><<<grid, 256, 0, s>>>(p, ngroups, nnt, pairs);
+    else k_gemm_i8<false, BM><<<grid, 256, 0, s>>>(p, ngroups, nnt, pairs);
 }
 
 }  // namespace
