@@ -10,9 +10,6 @@
 //     multiplied;
 //   * the BM x 128 token codes are gathered through registers into LDS,
 //     double-buffered, 16-byte chunks XOR-swizzled by row.
-// Workgroups are dealt over the 8 XCDs by their channel tile, and inside one
-// XCD the token tiles of a channel tile follow each other, so that an expert
-// with several token tiles fetches its weights once and reads the rest in L2.
 #include <type_traits>
 
 #include "i8_dev.h"
@@ -32,22 +29,36 @@ __device__ __forceinline__ i32x16 mfma_i8_32(u32x4 a, u32x4 b, i32x16 acc) {
 
 struct GemmTile {
     int e, n;            // expert (-1: none), channel tile
-    int64_t r0, m, m0;   // the expert's rows, the tile's first among them
+    int64_t r0;          // first row
+    int rows;            // at most BM
 };
 
-// Workgroup blk's tile: XCD blk % 8 owns the channel tiles n = xcd mod 8.
+// Workgroup blk's tile.  The list of tiles goes by expert, channel tile and
+// token tile (fastest); workgroups are dealt to the XCDs round-robin by the
+// hardware, and XCD x takes positions [kRun x, kRun (x + 1)) of every 8 kRun,
+// so that neighbours, which share weights or tokens, run beside each other on
+// one L2.
+constexpr int kRun = 8;
+
 template <int BM>
 __device__ __forceinline__ GemmTile find_tile(const I8Pass& A, int blk, int nnt, int lane) {
-    GemmTile g{-1, 0, 0, 0, 0};
-    const int xcd = blk & 7, slot = blk >> 3;
-    const int nn = (nnt - xcd + 7) / 8;
-    if (nn <= 0) return g;
+    GemmTile g{-1, 0, 0, 0};
+    const int pos = ((blk >> 3) / kRun * 8 + (blk & 7)) * kRun + (blk >> 3) % kRun;
+    // the i-th of nm tiles over m rows, all of nearly the same number
+    auto cut = [&](int64_t r0, int64_t m, int nm, int i) {
+        const int64_t per = (m + nm - 1) / nm;
+        g.r0 = r0 + i * per;
+        g.rows = (int)max((int64_t)0, min(per, m - i * per));
+    };
     if (!A.offsets) {
         const int nm = (int)((A.T + BM - 1) / BM);
-        if (slot / nm >= nn) return g;
-        return GemmTile{0, slot / nm * 8 + xcd, 0, A.T, (int64_t)(slot % nm) * BM};
+        if (pos / nm >= nnt) return g;
+        g.e = 0;
+        g.n = pos / nm;
+        cut(0, A.T, nm, pos % nm);
+        return g;
     }
-    const int want = slot / nn;
+    const int want = pos / nnt;
     int before = 0;
     for (int e0 = 0; e0 < A.E; e0 += 64) {
         const int e = e0 + lane;
@@ -66,12 +77,11 @@ __device__ __forceinline__ GemmTile find_tile(const I8Pass& A, int blk, int nnt,
             const uint64_t mask = __ballot(w >= incl - nm && w < incl);
             const int owner = __ffsll((unsigned long long)mask) - 1;
             const int nmo = __shfl(nm, owner);
-            const int r = slot - (before + __shfl(incl, owner) - nmo) * nn;
+            const int r = pos - (before + __shfl(incl, owner) - nmo) * nnt;
             g.e = e0 + owner;
-            g.r0 = __shfl(o0, owner);
-            g.m = __shfl(o1, owner) - g.r0;
-            g.n = r / nmo * 8 + xcd;
-            g.m0 = (int64_t)(r % nmo) * BM;
+            const int a = __shfl(o0, owner);
+            g.n = r / nmo;
+            cut(a, __shfl(o1, owner) - a, nmo, r % nmo);
             return g;
         }
         before += tot;
@@ -86,11 +96,11 @@ __global__ __launch_bounds__(256, 2) void k_gemm_i8(I8Pass A, int ngroups, int n
     __shared__ float qs[BM];
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
     const GemmTile t = find_tile<BM>(A, blockIdx.x, nnt, lane);
-    if (t.e < 0) return;
+    if (t.e < 0 || t.rows == 0) return;
     const int Kp = (A.K + kI8TileK - 1) / kI8TileK * kI8TileK;
     const int ns = (A.K + kStageK - 1) / kStageK;
-    const int left = (int)min((int64_t)BM, t.m - t.m0);   // rows of this tile
-    const int64_t first = t.r0 + t.m0;
+    const int left = t.rows;
+    const int64_t first = t.r0;
     auto source = [&](int row) -> int64_t {
         const int64_t r = first + min(row, left - 1);
         return A.offsets && A.perm_src ? A.perm_src[r] / A.k : r;
@@ -250,7 +260,7 @@ void launch(const I8Pass& p, bool pair, int ngroups, hipStream_t s) {
     const int nnt = (ngroups + 15) / 16;
     const int64_t rows = p.T * p.k;
     const int64_t nm = p.offsets ? rows / BM + (p.E < rows ? p.E : rows) : (p.T + BM - 1) / BM;
-    const unsigned grid = (unsigned)(8 * nm * ((nnt + 7) / 8));
+    const unsigned grid = (unsigned)round_up(nm * nnt, 8 * kRun);
     // two neighbouring channels in one store
     const uintptr_t two = p.out_dtype == MOE_DT_F32 ? 8 : 4;
     const bool pairs = p.N % 2 == 0 && p.ld_out % 2 == 0 &&
