@@ -104,6 +104,18 @@ __device__ __forceinline__ void store_f32(void* p, int dt, int64_t i, const floa
     }
 }
 
+// Four neighbours, aligned to four elements.
+__device__ __forceinline__ void store_quad(void* p, int dt, int64_t i, const float (&v)[4]) {
+    if (dt == MOE_DT_F32) {
+        *reinterpret_cast<f32x4*>(static_cast<float*>(p) + i) = f32x4{v[0], v[1], v[2], v[3]};
+    } else {
+        const bool b = dt == MOE_DT_BF16;
+        const uint2 u = {b ? pack_bf16(v[0], v[1]) : pack_f16(v[0], v[1]),
+                         b ? pack_bf16(v[2], v[3]) : pack_f16(v[2], v[3])};
+        *reinterpret_cast<uint2*>(static_cast<uint16_t*>(p) + i) = u;
+    }
+}
+
 __device__ __forceinline__ float wave_sum(float v) {
 #pragma unroll
     for (int off = 32; off >= 1; off >>= 1) v += __shfl_xor(v, off);

@@ -38,93 +38,146 @@ __device__ __forceinline__ Rows find_rows(const I8Pass& A, int s, int lane) {
             for (int i = 0; i < s - seen; ++i) m &= m - 1;
             const int owner = __ffsll((unsigned long long)m) - 1;
             const int a = __shfl(o0, owner), b = __shfl(o1, owner);
-            return Rows{e0 + owner, a, b - a};
+            return Rows{uniform(e0 + owner), uniform(a), uniform(b - a)};
         }
         seen += n;
     }
     return Rows{-1, 0, 0};
 }
 
-template <bool PAIR, int NG, int KS>
-__global__ __launch_bounds__(KS * 64) void k_i8(I8Pass A, int ngroups) {
-    __shared__ i32x4 part[KS][NG][64];
-    const int lane = threadIdx.x & 63, ks = threadIdx.x >> 6;
-    const Rows rw = find_rows(A, blockIdx.y, lane);
-    if (rw.e < 0) return;
+// A workgroup owns NG row groups of one matrix and its KS waves split the
+// inputs.  U input tiles are in flight per wave: a tile's registers are
+// reloaded as soon as it is multiplied.
+template <bool PAIR, int NG, int KS, int U>
+__global__ __launch_bounds__(KS * 64) void k_i8(I8Pass A, int ngroups, bool quads) {
+    __shared__ int32_t sums[KS > 1 ? NG * 256 : 1];
+    const int lane = threadIdx.x & 63, ks = uniform(threadIdx.x >> 6);
+    const Rows r = find_rows(A, blockIdx.y, lane);
+    if (r.e < 0) return;
     const int nkt = (A.K + kI8TileK - 1) / kI8TileK;      // tiles with weights
-    const int64_t gbytes = i8_tiles_k(A.K) * kI8TileBytes;
     const int g0 = blockIdx.x * NG;
+    const int k0 = nkt * ks / KS, k1 = nkt * (ks + 1) / KS;
     const uint8_t* w[NG];
 #pragma unroll
     for (int g = 0; g < NG; ++g)
-        w[g] = A.w + rw.e * A.w_stride + min(g0 + g, ngroups - 1) * gbytes +
-               lane * 16;
-    const float* sw = A.wscale + rw.e * A.wscale_stride;
-    const int k0 = (int)((int64_t)nkt * ks / KS), k1 = (int)((int64_t)nkt * (ks + 1) / KS);
+        w[g] = A.w + r.e * A.w_stride +
+               min(g0 + g, ngroups - 1) * (i8_tiles_k(A.K) * kI8TileBytes) + lane * 16;
+    const float* sw = A.wscale + r.e * A.wscale_stride;
 
-    for (int64_t c0 = (int64_t)blockIdx.z * 16; c0 < rw.m; c0 += (int64_t)gridDim.z * 16) {
-        const bool in = c0 + (lane & 15) < rw.m;
-        const int64_t row = rw.r0 + (in ? c0 + (lane & 15) : c0);
+    for (int64_t c0 = (int64_t)blockIdx.z * 16; c0 < r.m; c0 += (int64_t)gridDim.z * 16) {
+        const bool in = c0 + (lane & 15) < r.m;
+        const int64_t row = r.r0 + (in ? c0 + (lane & 15) : c0);
         const int64_t src = A.offsets && A.perm_src ? A.perm_src[row] / A.k : row;
         const int8_t* xq = A.q + src * A.ldq + (lane >> 4) * 16;
+        u32x4 wb[U][NG], xb[U];
+        auto load = [&](int u, int kt) {
+            const int64_t k = min(kt, k1 - 1);
+#pragma unroll
+            for (int g = 0; g < NG; ++g) wb[u][g] = load_stream16(w[g] + k * kI8TileBytes);
+            xb[u] = *reinterpret_cast<const u32x4*>(xq + k * kI8TileK);
+        };
         i32x4 acc[NG];
 #pragma unroll
         for (int g = 0; g < NG; ++g) acc[g] = i32x4{0, 0, 0, 0};
-        for (int kt = k0; kt < k1; ++kt) {
-            const u32x4 b = *reinterpret_cast<const u32x4*>(xq + (int64_t)kt * kI8TileK);
+        if (k0 < k1) {
 #pragma unroll
-            for (int g = 0; g < NG; ++g)
-                acc[g] = mfma_i8(load_stream16(w[g] + (int64_t)kt * kI8TileBytes), b, acc[g]);
-        }
+            for (int u = 0; u < U; ++u) load(u, k0 + u);
+            for (int kt = k0; kt < k1; kt += U) {
 #pragma unroll
-        for (int g = 0; g < NG; ++g) part[ks][g][lane] = acc[g];
-        __syncthreads();
-        if (ks == 0 && in) {
+                for (int u = 0; u < U; ++u) {
+                    if (kt + u < k1) {
 #pragma unroll
-            for (int g = 0; g < NG; ++g)
-                for (int i = 1; i < KS; ++i) acc[g] += part[i][g][lane];
-            const float sq = A.qscale[src];
-            if constexpr (PAIR) {
-#pragma unroll
-                for (int g = 0; g < NG; g += 2) {
-                    const int ch = (g0 + g) / 2 * 16 + (lane >> 4) * 4;
-                    float* h = static_cast<float*>(A.out) + row * A.ld_out;
-#pragma unroll
-                    for (int i = 0; i < 4; ++i)
-                        if (g0 + g < ngroups && ch + i < A.N)
-                            h[ch + i] = silu_mul(sq * sw[ch + i] * (float)acc[g][i],
-                                                 sq * sw[A.N + ch + i] * (float)acc[g + 1][i]);
-                }
-            } else {
-#pragma unroll
-                for (int g = 0; g < NG; ++g) {
-                    const int ch = (g0 + g) * 16 + (lane >> 4) * 4;
-#pragma unroll
-                    for (int i = 0; i < 4; ++i)
-                        if (g0 + g < ngroups && ch + i < A.N) {
-                            const float b = A.bias ? A.bias[ch + i] : 0.f;
-                            const float y[1] = {sq * sw[ch + i] * (float)acc[g][i] + b};
-                            store_f32<1>(A.out, A.out_dtype, row * A.ld_out + ch + i, y);
-                        }
+                        for (int g = 0; g < NG; ++g) acc[g] = mfma_i8(wb[u][g], xb[u], acc[g]);
+                    }
+                    load(u, kt + u + U);
                 }
             }
         }
-        __syncthreads();
+        if constexpr (KS > 1) {
+            // int32 sums over the input parts: the same bits in any order
+            if (ks == 0) {
+#pragma unroll
+                for (int g = 0; g < NG; ++g)
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) sums[(g * 4 + i) * 64 + lane] = acc[g][i];
+            }
+            __syncthreads();
+            if (ks > 0) {
+#pragma unroll
+                for (int g = 0; g < NG; ++g)
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+                        __hip_atomic_fetch_add(&sums[(g * 4 + i) * 64 + lane], acc[g][i],
+                                               __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_WORKGROUP);
+            }
+            __syncthreads();
+#pragma unroll
+            for (int g = 0; g < NG; ++g)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) acc[g][i] = sums[(g * 4 + i) * 64 + lane];
+        }
+        if (in) {
+            const float sq = A.qscale[src];
+#pragma unroll
+            for (int g = 0; g < NG; g += PAIR ? 2 : 1) {
+                // one wave writes a row group
+                if (g / (PAIR ? 2 : 1) % KS != ks || g0 + g >= ngroups) continue;
+                const int ch = (g0 + g) / (PAIR ? 2 : 1) * 16 + (lane >> 4) * 4;
+                float y[4];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const int c = min(ch + i, A.N - 1);
+                    if constexpr (PAIR)
+                        y[i] = silu_mul(sq * sw[c] * (float)acc[g][i],
+                                        sq * sw[A.N + c] * (float)acc[g + 1][i]);
+                    else
+                        y[i] = sq * sw[c] * (float)acc[g][i] + (A.bias ? A.bias[c] : 0.f);
+                }
+                const int64_t at = row * A.ld_out + ch;
+                if (quads) {
+                    if (ch < A.N) store_quad(A.out, A.out_dtype, at, y);
+                } else {
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const float y1[1] = {y[i]};
+                        if (ch + i < A.N) store_f32<1>(A.out, A.out_dtype, at + i, y1);
+                    }
+                }
+            }
+        }
+        if constexpr (KS > 1) __syncthreads();   // before the next chunk's sums
     }
+}
+
+template <bool PAIR, int NG, int KS, int U>
+void launch(const I8Pass& p, int ngroups, int64_t slots, int64_t mean, hipStream_t s) {
+    const uintptr_t four = p.out_dtype == MOE_DT_F32 ? 16 : 8;
+    const bool quads = p.N % 4 == 0 && p.ld_out % 4 == 0 &&
+                       reinterpret_cast<uintptr_t>(p.out) % four == 0;
+    // a workgroup takes its matrix's 16-row chunks in turn
+    const dim3 grid((unsigned)((ngroups + NG - 1) / NG), (unsigned)slots,
+                    (unsigned)(mean / 16 + (mean % 16 != 0)));
+    k_i8<PAIR, NG, KS, U><<<grid, KS * 64, 0, s>>>(p, ngroups, quads);
 }
 
 }  // namespace
 
 int launch_i8(const I8Pass& p, bool pair, void* stream) {
     hipStream_t s = reinterpret_cast<hipStream_t>(stream);
-    if ((p.offsets ? p.T * p.k / p.E : p.T) > 16) return launch_gemm_i8(p, pair, stream);
+    const int64_t rows = p.T * p.k, slots = p.offsets ? (p.E < rows ? p.E : rows) : 1;
+    const int64_t mean = rows / slots + (rows % slots != 0);    // rows of a matrix
+    if (mean > (slots > 1 ? 12 : 16)) return launch_gemm_i8(p, pair, stream);
     const int ngroups = (int)(round_up(p.N, 16) / 16) * (pair ? 2 : 1);
-    const int64_t slots = p.offsets ? (p.E < p.T * p.k ? p.E : p.T * p.k) : 1;
-    // a workgroup takes its matrix's 16-row chunks in turn
-    const int64_t rows = p.offsets ? p.T * p.k / p.E : p.T;
-    const dim3 grid((unsigned)((ngroups + 1) / 2), (unsigned)slots, (unsigned)(rows / 16 + 1));
-    if (pair) k_i8<true, 2, 4><<<grid, 256, 0, s>>>(p, ngroups);
-    else k_i8<false, 2, 4><<<grid, 256, 0, s>>>(p, ngroups);
+    const int64_t all = slots * ngroups;
+    if (pair) {
+        if (all >= 1024) launch<true, 2, 1, 8>(p, ngroups, slots, mean, s);
+        else if (all >= 256) launch<true, 2, 4, 8>(p, ngroups, slots, mean, s);
+        else launch<true, 2, 8, 4>(p, ngroups, slots, mean, s);
+    } else {
+        if (all >= 1024) launch<false, 2, 1, 8>(p, ngroups, slots, mean, s);
+        else if (all >= 256) launch<false, 2, 4, 8>(p, ngroups, slots, mean, s);
+        else launch<false, 1, 8, 4>(p, ngroups, slots, mean, s);
+    }
     MOEQ_CHECK_LAUNCH();
     return MOE_OK;
 }

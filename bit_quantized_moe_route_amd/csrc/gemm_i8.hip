@@ -71,17 +71,17 @@ __device__ __forceinline__ GemmTile find_tile(const I8Pass& A, int blk, int nnt,
             const int v = __shfl_up(incl, off);
             if (lane >= off) incl += v;
         }
-        const int tot = __shfl(incl, 63);
+        const int tot = __builtin_amdgcn_readlane(incl, 63);
         if (want < before + tot) {
             const int w = want - before;
             const uint64_t mask = __ballot(w >= incl - nm && w < incl);
-            const int owner = __ffsll((unsigned long long)mask) - 1;
-            const int nmo = __shfl(nm, owner);
-            const int r = pos - (before + __shfl(incl, owner) - nmo) * nnt;
+            const int owner = uniform(__ffsll((unsigned long long)mask) - 1);
+            const int nmo = __builtin_amdgcn_readlane(nm, owner);
+            const int r = pos - (before + __builtin_amdgcn_readlane(incl, owner) - nmo) * nnt;
             g.e = e0 + owner;
-            const int a = __shfl(o0, owner);
+            const int a = __builtin_amdgcn_readlane(o0, owner);
             g.n = r / nmo;
-            cut(a, __shfl(o1, owner) - a, nmo, r % nmo);
+            cut(a, __builtin_amdgcn_readlane(o1, owner) - a, nmo, r % nmo);
             return g;
         }
         before += tot;
@@ -89,16 +89,25 @@ __device__ __forceinline__ GemmTile find_tile(const I8Pass& A, int blk, int nnt,
     return g;
 }
 
-template <bool PAIR, int BM>
-__global__ __launch_bounds__(256, 2) void k_gemm_i8(I8Pass A, int ngroups, int nnt, bool pairs) {
+// CW waves side by side over the channels, 64 each; KP sets of them split the
+// inputs and add their int32 sums in LDS.
+template <bool PAIR, int BM, int CW, int KP>
+__global__ __launch_bounds__(64 * CW * KP, 2) void k_gemm_i8(I8Pass A, int ngroups, int nnt,
+                                                             bool pairs) {
     constexpr int NT = BM / 32;                  // 32-row token tiles
-    __shared__ __attribute__((aligned(1024))) uint8_t tok[2][BM * kStageK];
+    constexpr int XW = 4 / CW;                   // token loads of a wave per 32 rows
+    __shared__ __attribute__((aligned(1024))) uint8_t tokens[KP][2][BM * kStageK];
+    __shared__ int32_t sums[KP > 1 ? BM * 64 * CW : 1];
     __shared__ float qs[BM];
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    const int lane = threadIdx.x & 63, wave = uniform((threadIdx.x >> 6) % CW);
+    const int part = uniform((threadIdx.x >> 6) / CW);
+    auto& tok = tokens[part];
     const GemmTile t = find_tile<BM>(A, blockIdx.x, nnt, lane);
     if (t.e < 0 || t.rows == 0) return;
     const int Kp = (A.K + kI8TileK - 1) / kI8TileK * kI8TileK;
     const int ns = (A.K + kStageK - 1) / kStageK;
+    // this part's stages, and those of the longest part
+    const int sa = ns * part / KP, se = ns * (part + 1) / KP, steps = (ns + KP - 1) / KP;
     const int left = t.rows;
     const int64_t first = t.r0;
     auto source = [&](int row) -> int64_t {
@@ -107,17 +116,20 @@ __global__ __launch_bounds__(256, 2) void k_gemm_i8(I8Pass A, int ngroups, int n
     };
     if ((int)threadIdx.x < BM) qs[threadIdx.x] = A.qscale[source(threadIdx.x)];
 
-    // tokens: load i of a wave covers rows 32 i + 8 wave .. + 8 of the tile
-    const int8_t* xp[NT];
+    // tokens: load (i, h) of a wave covers rows 32 i + 8 (wave XW + h) .. + 8
+    const int8_t* xp[NT][XW];
 #pragma unroll
-    for (int i = 0; i < NT; ++i) xp[i] = A.q + source(32 * i + 8 * wave + (lane >> 3)) * A.ldq;
+    for (int i = 0; i < NT; ++i)
+#pragma unroll
+        for (int h = 0; h < XW; ++h)
+            xp[i][h] = A.q + source(32 * i + 8 * (wave * XW + h) + (lane >> 3)) * A.ldq;
     // chunk c of row r lies at chunk c ^ (r & 7): reads of 8 rows hit all banks
-    const int xat = wave * 8 * kStageK + (lane >> 3) * kStageK + ((lane & 7) ^ (lane >> 3)) * 16;
+    const int xat = (wave * XW * 8 + (lane >> 3)) * kStageK + ((lane & 7) ^ (lane >> 3)) * 16;
 
     // weights: tiles c = 0, 1 of this wave's 64 record rows; a lane's column is
     // channel lane & 31 of the gate (0) and up (1) rows, or, one matrix alone,
     // record row 2 (lane & 31) + c, so that a lane has two neighbours to store.
-    const int g0 = t.n * 16 + wave * 4;
+    const int g0 = (t.n * CW + wave) * 4;
     const int col = lane & 31;
     const uint8_t* wp[2];
 #pragma unroll
@@ -132,17 +144,22 @@ __global__ __launch_bounds__(256, 2) void k_gemm_i8(I8Pass A, int ngroups, int n
     // NB of the tile's 32-row token tiles hold rows
     auto run = [&](auto nb) {
         constexpr int NB = decltype(nb)::value;
-        u32x4 x[NB], w[2][4];
+        u32x4 x[NB][XW], w[2][4];
         auto load_tokens = [&](int s) {
             int k = s * kStageK + (lane & 7) * 16;
             if (k >= Kp) k = 0;                  // the weights there are zero
 #pragma unroll
-            for (int i = 0; i < NB; ++i) x[i] = *reinterpret_cast<const u32x4*>(xp[i] + k);
+            for (int i = 0; i < NB; ++i)
+#pragma unroll
+                for (int h = 0; h < XW; ++h)
+                    x[i][h] = *reinterpret_cast<const u32x4*>(xp[i][h] + k);
         };
         auto put_tokens = [&](int buf) {
 #pragma unroll
             for (int i = 0; i < NB; ++i)
-                *reinterpret_cast<u32x4*>(tok[buf] + i * 32 * kStageK + xat) = x[i];
+#pragma unroll
+                for (int h = 0; h < XW; ++h)
+                    *reinterpret_cast<u32x4*>(tok[buf] + (i * 32 + h * 8) * kStageK + xat) = x[i][h];
         };
         // The weights of input step j are reloaded for the next stage as soon as
         // they are multiplied: one set of registers, a whole stage of latency.
@@ -158,15 +175,15 @@ __global__ __launch_bounds__(256, 2) void k_gemm_i8(I8Pass A, int ngroups, int n
             for (int c = 0; c < 2; ++c)
 #pragma unroll
                 for (int v = 0; v < 16; ++v) acc[i][c][v] = 0;
-        load_tokens(0);
+        load_tokens(sa);
 #pragma unroll
-        for (int j = 0; j < 4; ++j) load_w(0, j);
+        for (int j = 0; j < 4; ++j) load_w(sa, j);
         put_tokens(0);
-        for (int s = 0; s < ns; ++s) {
+        for (int i0 = 0; i0 < steps; ++i0) {
             lds_barrier();
-            const int nx = min(s + 1, ns - 1);   // the last stage loads itself again
+            const int nx = min(sa + i0 + 1, ns - 1);   // the last stage loads one again
             load_tokens(nx);
-            const uint8_t* base = tok[s & 1] + col * kStageK;
+            const uint8_t* base = tok[i0 & 1] + col * kStageK;
             u32x4 a[2][NB];
             auto read_a = [&](int j) {
                 const int at = ((2 * j + (lane >> 5)) ^ (lane & 7)) * 16;
@@ -174,12 +191,13 @@ __global__ __launch_bounds__(256, 2) void k_gemm_i8(I8Pass A, int ngroups, int n
                 for (int i = 0; i < NB; ++i)
                     a[j & 1][i] = *reinterpret_cast<const u32x4*>(base + i * 32 * kStageK + at);
             };
+            if (KP > 1 && sa + i0 >= se) continue;     // a shorter part: only the barrier
             read_a(0);
             keep_order();
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
                 if (j < 3) read_a(j + 1);
-                else put_tokens((s + 1) & 1);
+                else put_tokens((i0 + 1) & 1);
 #pragma unroll
                 for (int i = 0; i < NB; ++i)
 #pragma unroll
@@ -190,12 +208,37 @@ __global__ __launch_bounds__(256, 2) void k_gemm_i8(I8Pass A, int ngroups, int n
 #pragma unroll
                 for (int i = 0; i < NB; ++i) {
                     if (j < 3) __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
-                    else __builtin_amdgcn_sched_group_barrier(0x200, 1, 0);
+                    else __builtin_amdgcn_sched_group_barrier(0x200, XW, 0);
                     __builtin_amdgcn_sched_group_barrier(0x008, 2, 0);
                 }
                 __builtin_amdgcn_sched_group_barrier(0x020, 2, 0);
                 keep_order();
             }
+        }
+        if constexpr (KP > 1) {
+            // int32 sums: the same bits in any order
+            int32_t* own = sums + wave * (BM * 64) + lane;
+            if (part == 0) {
+#pragma unroll
+                for (int i = 0; i < NB; ++i)
+#pragma unroll
+                    for (int c = 0; c < 2; ++c)
+#pragma unroll
+                        for (int v = 0; v < 16; ++v)
+                            own[((i * 2 + c) * 16 + v) * 64] = acc[i][c][v];
+            }
+            __syncthreads();
+            if (part > 0) {
+#pragma unroll
+                for (int i = 0; i < NB; ++i)
+#pragma unroll
+                    for (int c = 0; c < 2; ++c)
+#pragma unroll
+                        for (int v = 0; v < 16; ++v)
+                            __hip_atomic_fetch_add(&own[((i * 2 + c) * 16 + v) * 64], acc[i][c][v],
+                                                   __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_WORKGROUP);
+            }
+            __syncthreads();
         }
 
         // lane: rows 32 i + 8 (v >> 2) + 4 (lane >> 5) + (v & 3) of its column
@@ -205,7 +248,15 @@ __global__ __launch_bounds__(256, 2) void k_gemm_i8(I8Pass A, int ngroups, int n
 #pragma unroll
                 for (int v = 0; v < 16; ++v) {
                     const int row = 32 * i + 8 * (v >> 2) + 4 * (lane >> 5) + (v & 3);
-                    if (row < left) f(qs[row], acc[i][0][v], acc[i][1][v], (first + row) * A.ld_out);
+                    if (KP > 1 && v / (16 / KP) != part) continue;   // the parts share the rows
+                    if (row >= left) continue;
+                    if constexpr (KP > 1) {
+                        const int32_t* own = sums + wave * (BM * 64) + lane;
+                        f(qs[row], own[(i * 32 + v) * 64], own[(i * 32 + 16 + v) * 64],
+                          (first + row) * A.ld_out);
+                    } else {
+                        f(qs[row], acc[i][0][v], acc[i][1][v], (first + row) * A.ld_out);
+                    }
                 }
         };
         if constexpr (PAIR) {
@@ -255,18 +306,16 @@ __global__ __launch_bounds__(256, 2) void k_gemm_i8(I8Pass A, int ngroups, int n
     }
 }
 
-template <int BM>
-void launch(const I8Pass& p, bool pair, int ngroups, hipStream_t s) {
-    const int nnt = (ngroups + 15) / 16;
-    const int64_t rows = p.T * p.k;
-    const int64_t nm = p.offsets ? rows / BM + (p.E < rows ? p.E : rows) : (p.T + BM - 1) / BM;
+template <int BM, int CW, int KP>
+void launch(const I8Pass& p, bool pair, int ngroups, int64_t nm, hipStream_t s) {
+    const int nnt = (ngroups + 4 * CW - 1) / (4 * CW);
     const unsigned grid = (unsigned)round_up(nm * nnt, 8 * kRun);
     // two neighbouring channels in one store
     const uintptr_t two = p.out_dtype == MOE_DT_F32 ? 8 : 4;
     const bool pairs = p.N % 2 == 0 && p.ld_out % 2 == 0 &&
                        reinterpret_cast<uintptr_t>(p.out) % two == 0;
-    if (pair) k_gemm_i8<true, BM><<<grid, 256, 0, s>>>(p, ngroups, nnt, pairs);
-    else k_gemm_i8<false, BM><<<grid, 256, 0, s>>>(p, ngroups, nnt, pairs);
+    if (pair) k_gemm_i8<true, BM, CW, KP><<<grid, 64 * CW * KP, 0, s>>>(p, ngroups, nnt, pairs);
+    else k_gemm_i8<false, BM, CW, KP><<<grid, 64 * CW * KP, 0, s>>>(p, ngroups, nnt, pairs);
 }
 
 }  // namespace
@@ -274,10 +323,21 @@ void launch(const I8Pass& p, bool pair, int ngroups, hipStream_t s) {
 int launch_gemm_i8(const I8Pass& p, bool pair, void* stream) {
     hipStream_t s = reinterpret_cast<hipStream_t>(stream);
     const int ngroups = (int)(round_up(p.N, 16) / 16) * (pair ? 2 : 1);
-    const int64_t mean = p.offsets ? p.T * p.k / p.E : p.T;
-    if (mean > 64) launch<128>(p, pair, ngroups, s);
-    else if (mean > 32) launch<64>(p, pair, ngroups, s);
-    else launch<32>(p, pair, ngroups, s);
+    const int64_t rows = p.T * p.k, used = p.offsets ? (p.E < rows ? p.E : rows) : 1;
+    const int64_t mean = rows / used + (rows % used != 0);      // rows of a matrix
+    // The largest tile that still makes about a workgroup for every CU; a tile
+    // of twice a matrix's rows or more is no candidate.
+    auto tiles = [&](int bm) { return p.offsets ? rows / bm + used : (rows + bm - 1) / bm; };
+    auto fits = [&](int bm, int cw) {
+        return (bm == 32 || mean > bm / 2) &&
+               used * ((mean + bm - 1) / bm) * ((ngroups + 4 * cw - 1) / (4 * cw)) >= 160;
+    };
+    if (fits(128, 4)) launch<128, 4, 1>(p, pair, ngroups, tiles(128), s);
+    else if (fits(64, 4)) launch<64, 4, 1>(p, pair, ngroups, tiles(64), s);
+    else if (fits(64, 2)) launch<64, 2, 2>(p, pair, ngroups, tiles(64), s);
+    else if (fits(32, 4)) launch<32, 4, 1>(p, pair, ngroups, tiles(32), s);
+    else if (fits(32, 2)) launch<32, 2, 2>(p, pair, ngroups, tiles(32), s);
+    else launch<32, 1, 4>(p, pair, ngroups, tiles(32), s);
     MOEQ_CHECK_LAUNCH();
     return MOE_OK;
 }

@@ -21,6 +21,10 @@ __device__ __forceinline__ void keep_order() {
     __builtin_amdgcn_sched_barrier(0);
 }
 
+// A value that is the same in every lane, in a scalar register: what branches
+// around matrix instructions go by, which run whatever the lane mask says.
+__device__ __forceinline__ int uniform(int v) { return __builtin_amdgcn_readfirstlane(v); }
+
 __device__ __forceinline__ float silu_mul(float g, float u) { return g / (1.f + __expf(-g)) * u; }
 
 }  // namespace moeq
