@@ -9,8 +9,9 @@ several devices.
 """
 
 import ctypes
+import struct
 
-from . import _I32, _I64, _P, _check, _dptr, _stream, _torch, lib, route_permute
+from . import MOE_OK, _I32, _I64, _P, _check, _dptr, _torch, lib, route_permute
 
 DT_F32, DT_BF16, DT_F16, DT_I8 = 1, 2, 3, 4
 _F32 = ctypes.c_float
@@ -48,6 +49,12 @@ class BlockC(ctypes.Structure):
     ]
 
 
+# The same struct packed in one call: filling it field by field costs more than
+# the kernel of a small batch takes.
+_BLOCK = struct.Struct("@PqPPPqPPPqqPqPqPPqPqP7i4fi")
+assert _BLOCK.size == ctypes.sizeof(BlockC)
+
+
 class I8LinearC(ctypes.Structure):
     _fields_ = [("N", _I32), ("K", _I32), ("w", _P), ("w_scale", _P), ("bias", _P)]
 
@@ -61,7 +68,7 @@ class I8LayerC(ctypes.Structure):
 _C = ctypes.c_int
 _SZ = ctypes.c_size_t
 PROTOS = {
-    "moe_block_norm": (_C, [ctypes.POINTER(BlockC), _I64, _I32, _P]),
+    "moe_block_norm": (_C, [_P, _I64, _I32, _P]),
     "moe_quantize_i8": (_C, [_P, _I32, _I64, _I64, _I32, _P, _I64, _P, _P]),
     "moe_i8_matrix_bytes": (_SZ, [_I32, _I32]),
     "moe_i8_record_bytes": (_SZ, [_C, _I32, _I32]),
@@ -84,12 +91,14 @@ PROTOS = {
 
 def _rows(t, name, T, H, dev, dtype=None):
     """Checks rows [T, H] on dev; returns their stride in elements."""
-    if t.dim() != 2 or t.shape[0] != T or t.shape[1] != H:
+    if t.shape != (T, H):
         raise ValueError(f"{name} must be [{T}, {H}], got {list(t.shape)}")
     if t.device != dev:
         raise ValueError(f"{name} is on {t.device}, not on {dev}")
     if dtype is not None and t.dtype != dtype:
         raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
+    if t.is_contiguous():
+        return H
     s0, s1 = t.stride()
     if s1 != 1 and H > 1:
         raise ValueError(f"the elements of a row of {name} must lie side by side")
@@ -110,13 +119,34 @@ def _cuda(t, name):
     return t.device
 
 
+_fns = {}
+
+
+def _bind(L):
+    """The library's functions and torch's stream lookup (the raw one where
+    this torch has it: a Stream object costs as much as a launch)."""
+    torch = _torch()
+    _fns.clear()
+    _fns.update({n: getattr(L, n) for n in PROTOS})
+    _fns["lib"] = L
+    _fns["stream"] = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+        lambda i: torch.cuda.current_stream(i).cuda_stream)
+    _fns["device"] = torch.cuda.current_device
+
+
 def _call(name, dev, *args):
     """One library call on dev and its current stream."""
-    torch = _torch()
-    if dev.index != torch.cuda.current_device():
-        with torch.cuda.device(dev):
-            return _check(getattr(lib(), name)(*args, _stream(dev)), name)
-    return _check(getattr(lib(), name)(*args, _stream(dev)), name)
+    L = lib()
+    if _fns.get("lib") is not L:
+        _bind(L)
+    i = dev.index
+    if i == _fns["device"]():
+        st = _fns[name](*args, _fns["stream"](i))
+    else:
+        with _torch().cuda.device(dev):
+            st = _fns[name](*args, _fns["stream"](i))
+    if st != MOE_OK:
+        _check(st, name)
 
 
 def codes_width(K):
@@ -142,64 +172,66 @@ def _codes_like(T, K, q, scale, dev):
 # norms before and after a block
 # --------------------------------------------------------------------------
 
-def _vector(t, name, H, dev):
-    if t.dim() != 1 or t.shape[0] != H or t.device != dev or not t.is_contiguous():
+def _vector(t, name, H, dev, dtype=None):
+    if t.shape != (H,) or t.device != dev or not t.is_contiguous():
         raise ValueError(f"{name} must be [{H}], contiguous, on {dev}")
+    if dtype is not None and t.dtype != dtype:
+        raise ValueError("both norms' weights must be of one type")
     return t.data_ptr()
 
 
-def _block(dev, T, H, r, y, w, *, k=0, inv_perm=None, topk_w=None, y_shared=None, shared_gate=None,
+def _block(dev, T, H, r, y, w, k=0, inv_perm=None, topk_w=None, y_shared=None, shared_gate=None,
            post_w=None, gate=None, y_scale=1.0, r_scale=1.0, eps=1e-5, w_offset=0.0, r_out=None,
            out=None, out_dtype=None, codes=False, q=None, scale=None):
     torch = _torch()
-    b = BlockC(k=k, y_scale=y_scale, r_scale=r_scale, eps=eps, w_offset=w_offset)
+    y_p = y_ld = y_t = inv_p = tw_p = ys_p = ys_ld = ys_t = sg_p = 0
+    w_p = pw_p = w_t = g_p = g_ld = g_lh = g_t = 0
+    r_p = r_ld = r_t = ro_p = ro_ld = n_p = n_ld = n_t = q_p = q_ld = qs_p = 0
     if y is not None:
-        b.ld_y = _rows(y, "y_perm" if k else "y", T * (k or 1), H, dev)
-        b.y, b.y_dtype = y.data_ptr(), _dt(y.dtype)
+        y_ld = _rows(y, "y_perm" if k else "y", T * (k or 1), H, dev)
+        y_p, y_t = y.data_ptr(), _dt(y.dtype)
         if k:
-            b.inv_perm = _flat(inv_perm, "inv_perm", T * k, dev, torch.int32)
-            b.topk_w = _flat(topk_w, "topk_w", T * k, dev, torch.float32)
+            inv_p = _flat(inv_perm, "inv_perm", T * k, dev, torch.int32)
+            tw_p = _flat(topk_w, "topk_w", T * k, dev, torch.float32)
             if y_shared is not None:
-                b.ld_y_shared = _rows(y_shared, "y_shared", T, H, dev)
-                b.y_shared, b.y_shared_dtype = y_shared.data_ptr(), _dt(y_shared.dtype)
+                ys_ld = _rows(y_shared, "y_shared", T, H, dev)
+                ys_p, ys_t = y_shared.data_ptr(), _dt(y_shared.dtype)
             if shared_gate is not None:
-                b.shared_gate = _flat(shared_gate, "shared_gate", T, dev, torch.float32)
-    wt = w if w is not None else post_w
-    if wt is not None:
-        b.w_dtype = _dt(wt.dtype)
-        if w is not None and post_w is not None and w.dtype != post_w.dtype:
-            raise ValueError("both norms' weights must be of one type")
+                sg_p = _flat(shared_gate, "shared_gate", T, dev, torch.float32)
     if w is not None:
-        b.pre_w = _vector(w, "w", H, dev)
+        w_p, w_t = _vector(w, "w", H, dev), _dt(w.dtype)
     if post_w is not None:
-        b.post_w = _vector(post_w, "post_w", H, dev)
+        pw_p = _vector(post_w, "post_w", H, dev, None if w is None else w.dtype)
+        w_t = _dt(post_w.dtype)
     if gate is not None:
         if gate.dim() != 2 or gate.device != dev or gate.shape[0] not in (1, T) \
                 or gate.shape[1] not in (1, H) or (gate.shape[1] > 1 and gate.stride(1) != 1):
             raise ValueError(f"gate must be [{T}, 1], [1, {H}] or [{T}, {H}] on {dev}, the "
                              "elements of a row side by side")
-        b.gate, b.gate_dtype = gate.data_ptr(), _dt(gate.dtype)
-        b.gate_ld_t = gate.stride(0) if gate.shape[0] > 1 else 0
-        b.gate_ld_h = 1 if gate.shape[1] > 1 else 0
+        g_p, g_t = gate.data_ptr(), _dt(gate.dtype)
+        g_ld = gate.stride(0) if gate.shape[0] > 1 else 0
+        g_lh = 1 if gate.shape[1] > 1 else 0
     if r is not None:
-        b.ld_r = _rows(r, "r", T, H, dev)
-        b.r = r.data_ptr()
-        b.r_dtype = _dt(r.dtype)
+        r_ld = _rows(r, "r", T, H, dev)
+        r_p, r_t = r.data_ptr(), _dt(r.dtype)
     if r_out is not None:
-        b.ld_r_out = _rows(r_out, "r_out", T, H, dev, r.dtype if r is not None else None)
-        b.r_out, b.r_dtype = r_out.data_ptr(), _dt(r_out.dtype)
+        ro_ld = _rows(r_out, "r_out", T, H, dev, r.dtype if r is not None else None)
+        ro_p, r_t = r_out.data_ptr(), _dt(r_out.dtype)
     if out is None and w is not None:
         out = torch.empty((T, H), dtype=out_dtype or (r_out if r is None else r).dtype, device=dev)
     if out is False:
         out = None
     if out is not None:
-        b.ld_n = _rows(out, "out", T, H, dev, out_dtype)
-        b.n_out, b.n_dtype = out.data_ptr(), _dt(out.dtype)
+        n_ld = _rows(out, "out", T, H, dev, out_dtype)
+        n_p, n_t = out.data_ptr(), _dt(out.dtype)
     if codes:
-        q, b.ld_q, scale = _codes_like(T, H, q, scale, dev)
-        b.q_out, b.q_scale = q.data_ptr(), scale.data_ptr()
+        q, q_ld, scale = _codes_like(T, H, q, scale, dev)
+        q_p, qs_p = q.data_ptr(), scale.data_ptr()
     if T:
-        _call("moe_block_norm", dev, ctypes.byref(b), T, H)
+        _call("moe_block_norm", dev,
+              _BLOCK.pack(y_p, y_ld, inv_p, tw_p, ys_p, ys_ld, sg_p, pw_p, g_p, g_ld, g_lh, r_p,
+                          r_ld, ro_p, ro_ld, w_p, n_p, n_ld, q_p, q_ld, qs_p, k, y_t, ys_t, r_t,
+                          w_t, g_t, n_t, y_scale, r_scale, eps, w_offset, 0), T, H)
     return out, q, scale
 
 

@@ -64,24 +64,32 @@ size_t codes_ws(int64_t T, int32_t K) {
     return align_up((size_t)T * (size_t)round_up(K, kI8TileK)) + align_up((size_t)T * 4);
 }
 
-struct Codes {
-    const int8_t* q;
-    int64_t ldq;
-    const float* scale;
-};
-
-// The codes of x: x itself, or quantised into ws (codes_ws bytes).
-int take_codes(const void* x, int dt, int64_t ldx, const float* x_scale, int64_t T, int32_t K,
-               bool vec8, uint8_t* ws, void* stream, Codes& c) {
+// The rows of pass p: codes as they are; float rows handed to the kernel that
+// codes them itself, or coded into ws (codes_ws bytes) first.  T, k are the
+// batch's; n rows are here.
+int take_rows(I8Pass& p, const void* x, int dt, int64_t ldx, const float* x_scale, int64_t n,
+              bool vec8, uint8_t* ws, void* stream) {
+    p.x = nullptr;
     if (dt == MOE_DT_I8) {
-        c = Codes{static_cast<const int8_t*>(x), ldx, x_scale};
+        p.q = static_cast<const int8_t*>(x);
+        p.ldq = ldx;
+        p.qscale = x_scale;
         return MOE_OK;
     }
-    const int64_t ldq = round_up(K, kI8TileK);
+    if (i8_codes_itself(p.T, p.k, p.K, p.offsets != nullptr)) {
+        p.x = x;
+        p.ldx = ldx;
+        p.x_dtype = dt;
+        p.x_vec8 = vec8;
+        return MOE_OK;
+    }
+    const int64_t ldq = round_up(p.K, kI8TileK);
     int8_t* q = reinterpret_cast<int8_t*>(ws);
-    float* scale = reinterpret_cast<float*>(ws + align_up((size_t)T * (size_t)ldq));
-    c = Codes{q, ldq, scale};
-    return launch_quantize_i8(x, dt, ldx, T, K, q, ldq, scale, vec8, stream);
+    float* scale = reinterpret_cast<float*>(ws + align_up((size_t)n * (size_t)ldq));
+    p.q = q;
+    p.ldq = ldq;
+    p.qscale = scale;
+    return launch_quantize_i8(x, dt, ldx, n, p.K, q, ldq, scale, vec8, stream);
 }
 
 int check_linear(const std::string& fn, const moe_i8_linear* L) {
@@ -142,9 +150,6 @@ int run_ffn_i8(const std::string& fn, const moe_i8_layer* L, const void* x, int3
                     fn + ": workspace needs " + std::to_string(lay.total) + " bytes");
     if (!aligned(ws, kAlign)) return bad(fn, "workspace must be 256-byte aligned");
     uint8_t* w = static_cast<uint8_t*>(ws);
-    Codes c;
-    st = take_codes(x, x_dtype, ldx, x_scale, T, L->H, vec8, w, stream, c);
-    if (st) return st;
     const int64_t rows = T * k;
     float* h = reinterpret_cast<float*>(w + lay.h);
     I8Pass p{};
@@ -152,9 +157,6 @@ int run_ffn_i8(const std::string& fn, const moe_i8_layer* L, const void* x, int3
     p.w_stride = L->w13_stride;
     p.wscale = L->w13_scale;
     p.wscale_stride = 2 * (int64_t)L->I;
-    p.q = c.q;
-    p.ldq = c.ldq;
-    p.qscale = c.scale;
     p.offsets = offsets;
     p.perm_src = perm_src;
     p.T = T;
@@ -165,24 +167,22 @@ int run_ffn_i8(const std::string& fn, const moe_i8_layer* L, const void* x, int3
     p.out = h;
     p.ld_out = L->I;
     p.out_dtype = MOE_DT_F32;
-    st = launch_i8(p, true, stream);
+    st = take_rows(p, x, x_dtype, ldx, x_scale, T, vec8, w, stream);
     if (st) return st;
-    Codes hc;
-    st = take_codes(h, MOE_DT_F32, L->I, nullptr, rows, L->I, L->I % 8 == 0, w + lay.hq, stream, hc);
+    st = launch_i8(p, true, stream);
     if (st) return st;
     p.w = static_cast<const uint8_t*>(L->w2);
     p.w_stride = L->w2_stride;
     p.wscale = L->w2_scale;
     p.wscale_stride = L->H;
-    p.q = hc.q;
-    p.ldq = hc.ldq;
-    p.qscale = hc.scale;
     p.perm_src = nullptr;
     p.N = L->H;
     p.K = L->I;
     p.out = y;
     p.ld_out = L->H;
     p.out_dtype = y_dtype;
+    st = take_rows(p, h, MOE_DT_F32, L->I, nullptr, rows, L->I % 8 == 0, w + lay.hq, stream);
+    if (st) return st;
     return launch_i8(p, false, stream);
 }
 
@@ -317,17 +317,10 @@ int moe_linear_i8(const moe_i8_linear* linear, const void* x, int32_t x_dtype, i
             return fail(MOE_EWORKSPACE, fn + ": workspace needs " + std::to_string(need) + " bytes");
         if (!aligned(ws, kAlign)) return bad(fn, "workspace must be 256-byte aligned");
     }
-    Codes c;
-    st = take_codes(x, x_dtype, ldx, x_scale, T, linear->K, vec8, static_cast<uint8_t*>(ws),
-                    stream, c);
-    if (st) return st;
     I8Pass p{};
     p.w = static_cast<const uint8_t*>(linear->w);
     p.wscale = linear->w_scale;
     p.bias = linear->bias;
-    p.q = c.q;
-    p.ldq = c.ldq;
-    p.qscale = c.scale;
     p.T = T;
     p.E = p.k = 1;
     p.N = linear->N;
@@ -335,6 +328,8 @@ int moe_linear_i8(const moe_i8_linear* linear, const void* x, int32_t x_dtype, i
     p.out = out;
     p.ld_out = ldo;
     p.out_dtype = out_dtype;
+    st = take_rows(p, x, x_dtype, ldx, x_scale, T, vec8, static_cast<uint8_t*>(ws), stream);
+    if (st) return st;
     return launch_i8(p, false, stream);
 }
 

@@ -23,128 +23,164 @@ struct BlockRow {
     int H, nw;
 };
 
-template <int V, int NCH, bool COMB>
+// COMB: slots of the gated sum that are in flight together, 0: y is a row.
+// Everything the row needs is loaded before the first reduction (EARLY), while
+// it fits the registers of a workgroup of 1024 threads.
+template <int V, int NCH, int COMB>
 __global__ __launch_bounds__(1024) void k_block(BlockRow A) {
+    constexpr bool EARLY = V * NCH <= 8;
+    constexpr int NE = EARLY ? NCH : 1;
     __shared__ float red[3][16];
     const moe_block& b = A.b;
     const int64_t t = blockIdx.x;
     const int H = A.H, nt = A.nw * 64;
+    const bool has_y = COMB || b.y;
     float v[NCH][V];
+    Raw<V> rr[NE], rp[NE], rg[NE], rn[NE];
+    // threads past the row read its start and hold zeros
+    auto place = [&](int c) { return (c * nt + (int)threadIdx.x) * V; };
+    auto at = [&](int c) { return place(c) < H ? place(c) : 0; };
+    auto load_r = [&](int c, Raw<V>& x) { if (b.r) x.load(b.r, b.r_dtype, t * b.ld_r + at(c)); };
+    auto load_p = [&](int c, Raw<V>& x) { if (b.post_w) x.load(b.post_w, b.w_dtype, at(c)); };
+    auto load_g = [&](int c, Raw<V>& x) {
+        if (b.gate && b.gate_ld_h) x.load(b.gate, b.gate_dtype, t * b.gate_ld_t + at(c));
+    };
+    auto load_n = [&](int c, Raw<V>& x) { if (b.pre_w) x.load(b.pre_w, b.w_dtype, at(c)); };
+    const float gate1 = b.gate && !b.gate_ld_h ? load_elem(b.gate, b.gate_dtype, t * b.gate_ld_t)
+                                               : 1.f;
 
     // ------------------------------------------------ the block's output
-    if constexpr (COMB) {
-        const float sg = b.y_shared && b.shared_gate ? b.shared_gate[t] : 1.f;
+    Raw<V> ry[NCH];
+    if constexpr (COMB == 0) {
+        if (b.y) {
+#pragma unroll
+            for (int c = 0; c < NCH; ++c) ry[c].load(b.y, b.y_dtype, t * b.ld_y + at(c));
+        }
+    } else if (b.y_shared) {
+#pragma unroll
+        for (int c = 0; c < NCH; ++c)
+            ry[c].load(b.y_shared, b.y_shared_dtype, t * b.ld_y_shared + at(c));
+    }
+    if constexpr (EARLY) {
 #pragma unroll
         for (int c = 0; c < NCH; ++c) {
-            const int h = (c * nt + (int)threadIdx.x) * V;
+            load_r(c, rr[c]);
+            load_p(c, rp[c]);
+            load_g(c, rg[c]);
+            load_n(c, rn[c]);
+        }
+    }
 #pragma unroll
-            for (int e = 0; e < V; ++e) v[c][e] = 0.f;
-            if (h >= H) continue;
-            for (int j = 0; j < b.k; ++j) {
-                const int64_t row = b.inv_perm[t * b.k + j];
-                const float wj = b.topk_w[t * b.k + j];
-                float y[V];
-                load_f32<V>(b.y, b.y_dtype, row * b.ld_y + h, y);
+    for (int c = 0; c < NCH; ++c)
 #pragma unroll
-                for (int e = 0; e < V; ++e) v[c][e] += wj * y[e];
+        for (int e = 0; e < V; ++e) v[c][e] = 0.f;
+    if constexpr (COMB > 0) {
+        for (int j0 = 0; j0 < b.k; j0 += COMB) {
+            int64_t row[COMB];
+            float wj[COMB];
+#pragma unroll
+            for (int u = 0; u < COMB; ++u) {
+                const int64_t a = t * b.k + min(j0 + u, b.k - 1);
+                row[u] = b.inv_perm[a] * b.ld_y;
+                wj[u] = b.topk_w[a];
             }
-            if (b.y_shared) {
-                float y[V];
-                load_f32<V>(b.y_shared, b.y_shared_dtype, t * b.ld_y_shared + h, y);
 #pragma unroll
-                for (int e = 0; e < V; ++e) v[c][e] += sg * y[e];
+            for (int c = 0; c < NCH; ++c) {
+                Raw<V> y[COMB];
+#pragma unroll
+                for (int u = 0; u < COMB; ++u) y[u].load(b.y, b.y_dtype, row[u] + at(c));
+#pragma unroll
+                for (int u = 0; u < COMB; ++u) {
+                    if (j0 + u >= b.k) break;
+                    float f[V];
+                    y[u].f32(b.y_dtype, f);
+#pragma unroll
+                    for (int e = 0; e < V; ++e) v[c][e] += wj[u] * f[e];
+                }
+            }
+        }
+        if (b.y_shared) {
+            const float sg = b.shared_gate ? b.shared_gate[t] : 1.f;
+#pragma unroll
+            for (int c = 0; c < NCH; ++c) {
+                float f[V];
+                ry[c].f32(b.y_shared_dtype, f);
+#pragma unroll
+                for (int e = 0; e < V; ++e) v[c][e] += sg * f[e];
             }
         }
     } else if (b.y) {
 #pragma unroll
-        for (int c = 0; c < NCH; ++c) {
-            const int h = (c * nt + (int)threadIdx.x) * V;
-            if (h < H) {
-                load_f32<V>(b.y, b.y_dtype, t * b.ld_y + h, v[c]);
-            } else {
-#pragma unroll
-                for (int e = 0; e < V; ++e) v[c][e] = 0.f;
-            }
-        }
+        for (int c = 0; c < NCH; ++c) ry[c].f32(b.y_dtype, v[c]);
     }
 
     // ------------------------------------------------ the norm after
-    const bool has_y = COMB || b.y;
-    float rstd = 1.f;
-    if (has_y && b.post_w) {
+    auto norm = [&](float* r) {
         float ss = 0.f;
 #pragma unroll
         for (int c = 0; c < NCH; ++c)
+            if (place(c) < H)
 #pragma unroll
-            for (int e = 0; e < V; ++e) ss += v[c][e] * v[c][e];
-        ss = block_sum(ss, red[0], A.nw);
-        rstd = 1.f / sqrtf(ss / (float)H + b.eps);
-    }
+                for (int e = 0; e < V; ++e) ss += v[c][e] * v[c][e];
+        ss = block_sum(ss, r, A.nw);
+        return 1.f / sqrtf(ss / (float)H + b.eps);
+    };
+    float rstd = 1.f;
+    if (has_y && b.post_w) rstd = norm(red[0]);
 
     // ------------------------------------------------ gate, scales, residual
 #pragma unroll
     for (int c = 0; c < NCH; ++c) {
-        const int h = (c * nt + (int)threadIdx.x) * V;
-        if (h >= H) {
-#pragma unroll
-            for (int e = 0; e < V; ++e) v[c][e] = 0.f;
-            continue;
+        constexpr bool E = EARLY;
+        Raw<V>& xr = rr[E ? c : 0];
+        Raw<V>& xp = rp[E ? c : 0];
+        Raw<V>& xg = rg[E ? c : 0];
+        if constexpr (!E) {
+            load_r(c, xr);
+            load_p(c, xp);
+            load_g(c, xg);
         }
         if (has_y) {
+            float f[V];
             if (b.post_w) {
-                float w[V];
-                load_f32<V>(b.post_w, b.w_dtype, h, w);
+                xp.f32(b.w_dtype, f);
 #pragma unroll
-                for (int e = 0; e < V; ++e) v[c][e] = v[c][e] * rstd * (b.w_offset + w[e]);
+                for (int e = 0; e < V; ++e) v[c][e] = v[c][e] * rstd * (b.w_offset + f[e]);
             }
             if (b.gate) {
-                float g[V];
-                if (b.gate_ld_h) {
-                    load_f32<V>(b.gate, b.gate_dtype, t * b.gate_ld_t + h, g);
-                } else {
-                    const float g1 = load_elem(b.gate, b.gate_dtype, t * b.gate_ld_t);
+                if (b.gate_ld_h) xg.f32(b.gate_dtype, f);
 #pragma unroll
-                    for (int e = 0; e < V; ++e) g[e] = g1;
-                }
-#pragma unroll
-                for (int e = 0; e < V; ++e) v[c][e] *= g[e];
+                for (int e = 0; e < V; ++e) v[c][e] *= b.gate_ld_h ? f[e] : gate1;
             }
 #pragma unroll
             for (int e = 0; e < V; ++e) v[c][e] *= b.y_scale;
         }
         if (b.r) {
-            float r[V];
-            load_f32<V>(b.r, b.r_dtype, t * b.ld_r + h, r);
+            float f[V];
+            xr.f32(b.r_dtype, f);
 #pragma unroll
             for (int e = 0; e < V; ++e)
-                v[c][e] = has_y ? b.r_scale * r[e] + v[c][e] : b.r_scale * r[e];
+                v[c][e] = has_y ? b.r_scale * f[e] + v[c][e] : b.r_scale * f[e];
         }
-        if (b.r_out) store_f32<V>(b.r_out, b.r_dtype, t * b.ld_r_out + h, v[c]);
+        if (b.r_out && place(c) < H) store_f32<V>(b.r_out, b.r_dtype, t * b.ld_r_out + place(c), v[c]);
     }
     if (!b.n_out && !b.q_out) return;
 
     // ------------------------------------------------ the norm before the next
-    if (b.pre_w) {
-        float ss = 0.f;
-#pragma unroll
-        for (int c = 0; c < NCH; ++c)
-#pragma unroll
-            for (int e = 0; e < V; ++e) ss += v[c][e] * v[c][e];
-        ss = block_sum(ss, red[1], A.nw);
-        rstd = 1.f / sqrtf(ss / (float)H + b.eps);
-    }
+    if (b.pre_w) rstd = norm(red[1]);
     uint32_t amax = 0u;
 #pragma unroll
     for (int c = 0; c < NCH; ++c) {
-        const int h = (c * nt + (int)threadIdx.x) * V;
-        if (h >= H) continue;
+        Raw<V>& xn = rn[EARLY ? c : 0];
+        if constexpr (!EARLY) load_n(c, xn);
         if (b.pre_w) {
-            float w[V];
-            load_f32<V>(b.pre_w, b.w_dtype, h, w);
+            float f[V];
+            xn.f32(b.w_dtype, f);
 #pragma unroll
-            for (int e = 0; e < V; ++e) v[c][e] = v[c][e] * rstd * (b.w_offset + w[e]);
+            for (int e = 0; e < V; ++e) v[c][e] = v[c][e] * rstd * (b.w_offset + f[e]);
         }
-        if (b.n_out) store_f32<V>(b.n_out, b.n_dtype, t * b.ld_n + h, v[c]);
+        if (place(c) >= H) continue;
+        if (b.n_out) store_f32<V>(b.n_out, b.n_dtype, t * b.ld_n + place(c), v[c]);
 #pragma unroll
         for (int e = 0; e < V; ++e) amax = max(amax, __float_as_uint(v[c][e]) & 0x7fffffffu);
     }
@@ -157,7 +193,7 @@ __global__ __launch_bounds__(1024) void k_block(BlockRow A) {
     int8_t* q = b.q_out + t * b.ld_q;
 #pragma unroll
     for (int c = 0; c < NCH; ++c) {
-        const int h = (c * nt + (int)threadIdx.x) * V;
+        const int h = place(c);
         if (h >= H) continue;
         if constexpr (V == 8) {
             const uint2 u = {pack_codes4(&v[c][0], rc.mul), pack_codes4(&v[c][4], rc.mul)};
@@ -173,10 +209,11 @@ __global__ __launch_bounds__(1024) void k_block(BlockRow A) {
 
 template <int V, int NCH>
 void launch(const BlockRow& A, int64_t T, hipStream_t s) {
+    constexpr int C = V == 1 && NCH > 8 ? 2 : 4;
     if (A.b.k > 0)
-        k_block<V, NCH, true><<<(unsigned)T, A.nw * 64, 0, s>>>(A);
+        k_block<V, NCH, C><<<(unsigned)T, A.nw * 64, 0, s>>>(A);
     else
-        k_block<V, NCH, false><<<(unsigned)T, A.nw * 64, 0, s>>>(A);
+        k_block<V, NCH, 0><<<(unsigned)T, A.nw * 64, 0, s>>>(A);
 }
 
 }  // namespace

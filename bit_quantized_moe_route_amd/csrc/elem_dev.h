@@ -55,7 +55,31 @@ __device__ __forceinline__ float load_elem(const void* p, int dt, int64_t i) {
     return (float)__builtin_bit_cast(_Float16, u);
 }
 
-// V elements (8: one aligned vector, 1: a scalar) as fp32.
+// V elements (8: one aligned vector, 1: a scalar) as loaded, and as fp32.
+template <int V>
+struct Raw;
+template <>
+struct Raw<8> {
+    Raw8 r;
+    __device__ __forceinline__ void load(const void* p, int dt, int64_t i) {
+        r = load_raw8(p, dt, i);
+    }
+    __device__ __forceinline__ void f32(int dt, float (&v)[8]) const { raw_to_f32(r, dt, v); }
+};
+template <>
+struct Raw<1> {
+    uint32_t r;
+    __device__ __forceinline__ void load(const void* p, int dt, int64_t i) {
+        r = dt == MOE_DT_F32 ? static_cast<const uint32_t*>(p)[i]
+                             : static_cast<const uint16_t*>(p)[i];
+    }
+    __device__ __forceinline__ void f32(int dt, float (&v)[1]) const {
+        v[0] = dt == MOE_DT_F32    ? __uint_as_float(r)
+               : dt == MOE_DT_BF16 ? __uint_as_float(r << 16)
+                                   : (float)__builtin_bit_cast(_Float16, (uint16_t)r);
+    }
+};
+
 template <int V>
 __device__ __forceinline__ void load_f32(const void* p, int dt, int64_t i, float (&v)[V]) {
     if constexpr (V == 8) {

@@ -8,6 +8,8 @@
 // 16-byte load per lane) by up to 16 token rows (B: gathered 16-byte loads
 // from the caches).  The KS waves of a workgroup split the inputs and add
 // their int32 sums in LDS (integer sums: any order gives the same bits).
+#include <type_traits>
+
 #include "i8_dev.h"
 
 namespace moeq {
@@ -45,12 +47,62 @@ __device__ __forceinline__ Rows find_rows(const I8Pass& A, int s, int lane) {
     return Rows{-1, 0, 0};
 }
 
+// Codes row `src` of A.x into LDS, zeros from K to `width`; two passes over the
+// row, the second from the caches.
+template <int KS>
+__device__ __forceinline__ void code_row(const I8Pass& A, int64_t src, int8_t* q, float* scale,
+                                         uint32_t* red, int width) {
+    const int tid = threadIdx.x;
+    const int64_t at = src * A.ldx;
+    uint32_t amax = 0u;
+    auto each = [&](auto&& f) {
+        if (A.x_vec8) {
+            for (int h = tid * 8; h < A.K; h += KS * 64 * 8) {
+                float v[8];
+                load_f32<8>(A.x, A.x_dtype, at + h, v);
+                f(h, v, std::integral_constant<int, 8>{});
+            }
+        } else {
+            for (int h = tid; h < A.K; h += KS * 64) {
+                float v[1];
+                load_f32<1>(A.x, A.x_dtype, at + h, v);
+                f(h, v, std::integral_constant<int, 1>{});
+            }
+        }
+    };
+    each([&](int, const float* v, auto n) {
+#pragma unroll
+        for (int e = 0; e < decltype(n)::value; ++e)
+            amax = max(amax, __float_as_uint(v[e]) & 0x7fffffffu);
+    });
+    amax = block_max(amax, red, KS);
+    const RowCode rc = row_code(amax);
+    if (tid == 0) *scale = rc.scale;
+    each([&](int h, const float* v, auto n) {
+        if constexpr (decltype(n)::value == 8)
+            *reinterpret_cast<uint2*>(q + h) =
+                uint2{pack_codes4(v, rc.mul), pack_codes4(v + 4, rc.mul)};
+        else
+            q[h] = (int8_t)code_of(v[0], rc.mul);
+    });
+    for (int h = A.K + tid; h < width; h += KS * 64) q[h] = 0;
+    if constexpr (KS > 1) __syncthreads();   // red is free again
+}
+
 // A workgroup owns NG row groups of one matrix and its KS waves split the
 // inputs.  U input tiles are in flight per wave: a tile's registers are
 // reloaded as soon as it is multiplied.
-template <bool PAIR, int NG, int KS, int U>
+//
+// XR > 0: the rows come uncoded (A.x, of A.x_dtype) and every workgroup codes
+// the XR rows it multiplies in LDS, behind its first weight loads, which saves
+// a launch where there are few of them.
+template <bool PAIR, int NG, int KS, int U, int XR>
 __global__ __launch_bounds__(KS * 64) void k_i8(I8Pass A, int ngroups, bool quads) {
+    constexpr int ROWS = XR ? XR : 16;                    // token rows of a chunk
     __shared__ int32_t sums[KS > 1 ? NG * 256 : 1];
+    __shared__ float xscale[XR ? XR : 1];
+    __shared__ uint32_t red[KS];
+    extern __shared__ __attribute__((aligned(16))) int8_t xcodes[];   // XR rows of nkt tiles
     const int lane = threadIdx.x & 63, ks = uniform(threadIdx.x >> 6);
     const Rows r = find_rows(A, blockIdx.y, lane);
     if (r.e < 0) return;
@@ -64,17 +116,23 @@ __global__ __launch_bounds__(KS * 64) void k_i8(I8Pass A, int ngroups, bool quad
                min(g0 + g, ngroups - 1) * (i8_tiles_k(A.K) * kI8TileBytes) + lane * 16;
     const float* sw = A.wscale + r.e * A.wscale_stride;
 
-    for (int64_t c0 = (int64_t)blockIdx.z * 16; c0 < r.m; c0 += (int64_t)gridDim.z * 16) {
-        const bool in = c0 + (lane & 15) < r.m;
-        const int64_t row = r.r0 + (in ? c0 + (lane & 15) : c0);
-        const int64_t src = A.offsets && A.perm_src ? A.perm_src[row] / A.k : row;
-        const int8_t* xq = A.q + src * A.ldq + (lane >> 4) * 16;
+    for (int64_t c0 = (int64_t)blockIdx.z * ROWS; c0 < r.m; c0 += (int64_t)gridDim.z * ROWS) {
+        const int left = (int)min((int64_t)ROWS, r.m - c0);
+        const bool in = (lane & 15) < left;
+        const int64_t row = r.r0 + c0 + (in ? lane & 15 : 0);
+        auto source = [&](int64_t i) {
+            return A.offsets && A.perm_src ? (int64_t)(A.perm_src[i] / A.k) : i;
+        };
+        const int64_t src = source(row);
+        const int8_t* xq = XR ? xcodes + (in ? lane & 15 : 0) * (nkt * kI8TileK)
+                              : A.q + src * A.ldq;
+        xq += (lane >> 4) * 16;
         u32x4 wb[U][NG], xb[U];
         auto load = [&](int u, int kt) {
             const int64_t k = min(kt, k1 - 1);
 #pragma unroll
             for (int g = 0; g < NG; ++g) wb[u][g] = load_stream16(w[g] + k * kI8TileBytes);
-            xb[u] = *reinterpret_cast<const u32x4*>(xq + k * kI8TileK);
+            if constexpr (!XR) xb[u] = *reinterpret_cast<const u32x4*>(xq + k * kI8TileK);
         };
         i32x4 acc[NG];
 #pragma unroll
@@ -82,10 +140,20 @@ __global__ __launch_bounds__(KS * 64) void k_i8(I8Pass A, int ngroups, bool quad
         if (k0 < k1) {
 #pragma unroll
             for (int u = 0; u < U; ++u) load(u, k0 + u);
+        }
+        if constexpr (XR > 0) {
+            for (int i = 0; i < left; ++i)
+                code_row<KS>(A, source(r.r0 + c0 + i), xcodes + i * (nkt * kI8TileK), xscale + i,
+                             red, nkt * kI8TileK);
+            __syncthreads();
+        }
+        if (k0 < k1) {
             for (int kt = k0; kt < k1; kt += U) {
 #pragma unroll
                 for (int u = 0; u < U; ++u) {
                     if (kt + u < k1) {
+                        if constexpr (XR > 0)
+                            xb[u] = *reinterpret_cast<const u32x4*>(xq + (kt + u) * kI8TileK);
 #pragma unroll
                         for (int g = 0; g < NG; ++g) acc[g] = mfma_i8(wb[u][g], xb[u], acc[g]);
                     }
@@ -117,7 +185,7 @@ __global__ __launch_bounds__(KS * 64) void k_i8(I8Pass A, int ngroups, bool quad
                 for (int i = 0; i < 4; ++i) acc[g][i] = sums[(g * 4 + i) * 64 + lane];
         }
         if (in) {
-            const float sq = A.qscale[src];
+            const float sq = XR ? xscale[lane & 15] : A.qscale[src];
 #pragma unroll
             for (int g = 0; g < NG; g += PAIR ? 2 : 1) {
                 // one wave writes a row group
@@ -145,38 +213,52 @@ __global__ __launch_bounds__(KS * 64) void k_i8(I8Pass A, int ngroups, bool quad
                 }
             }
         }
-        if constexpr (KS > 1) __syncthreads();   // before the next chunk's sums
+        if constexpr (KS > 1 || XR > 0) __syncthreads();   // before the next chunk
     }
 }
 
-template <bool PAIR, int NG, int KS, int U>
+template <bool PAIR, int NG, int KS, int U, int XR>
 void launch(const I8Pass& p, int ngroups, int64_t slots, int64_t mean, hipStream_t s) {
     const uintptr_t four = p.out_dtype == MOE_DT_F32 ? 16 : 8;
     const bool quads = p.N % 4 == 0 && p.ld_out % 4 == 0 &&
                        reinterpret_cast<uintptr_t>(p.out) % four == 0;
-    // a workgroup takes its matrix's 16-row chunks in turn
+    // a workgroup takes its matrix's chunks of rows in turn
+    constexpr int ROWS = XR ? XR : 16;
     const dim3 grid((unsigned)((ngroups + NG - 1) / NG), (unsigned)slots,
-                    (unsigned)(mean / 16 + (mean % 16 != 0)));
-    k_i8<PAIR, NG, KS, U><<<grid, KS * 64, 0, s>>>(p, ngroups, quads);
+                    (unsigned)((mean + ROWS - 1) / ROWS));
+    k_i8<PAIR, NG, KS, U, XR><<<grid, KS * 64, XR * round_up(p.K, kI8TileK), s>>>(p, ngroups,
+                                                                                 quads);
+}
+
+template <bool PAIR, int XR>
+void pick(const I8Pass& p, int ngroups, int64_t slots, int64_t mean, hipStream_t s) {
+    const int64_t all = slots * ngroups;
+    if (all >= 1024) launch<PAIR, 2, 1, 8, XR>(p, ngroups, slots, mean, s);
+    else if (all >= 256) launch<PAIR, 2, 4, 8, XR>(p, ngroups, slots, mean, s);
+    else launch<PAIR, PAIR ? 2 : 1, 8, 4, XR>(p, ngroups, slots, mean, s);
 }
 
 }  // namespace
+
+bool i8_codes_itself(int64_t T, int32_t k, int32_t K, bool routed) {
+    return T * k <= (routed ? 16 : 4) && (routed ? 1 : T) * round_up(K, kI8TileK) <= 24576;
+}
 
 int launch_i8(const I8Pass& p, bool pair, void* stream) {
     hipStream_t s = reinterpret_cast<hipStream_t>(stream);
     const int64_t rows = p.T * p.k, slots = p.offsets ? (p.E < rows ? p.E : rows) : 1;
     const int64_t mean = rows / slots + (rows % slots != 0);    // rows of a matrix
-    if (mean > (slots > 1 ? 12 : 16)) return launch_gemm_i8(p, pair, stream);
     const int ngroups = (int)(round_up(p.N, 16) / 16) * (pair ? 2 : 1);
-    const int64_t all = slots * ngroups;
-    if (pair) {
-        if (all >= 1024) launch<true, 2, 1, 8>(p, ngroups, slots, mean, s);
-        else if (all >= 256) launch<true, 2, 4, 8>(p, ngroups, slots, mean, s);
-        else launch<true, 2, 8, 4>(p, ngroups, slots, mean, s);
+    if (p.x) {
+        const bool one = p.offsets || p.T == 1;
+        if (one && pair) pick<true, 1>(p, ngroups, slots, mean, s);
+        else if (one) pick<false, 1>(p, ngroups, slots, mean, s);
+        else if (pair) pick<true, 4>(p, ngroups, slots, mean, s);
+        else pick<false, 4>(p, ngroups, slots, mean, s);
     } else {
-        if (all >= 1024) launch<false, 2, 1, 8>(p, ngroups, slots, mean, s);
-        else if (all >= 256) launch<false, 2, 4, 8>(p, ngroups, slots, mean, s);
-        else launch<false, 1, 8, 4>(p, ngroups, slots, mean, s);
+        if (mean > (slots > 1 ? 12 : 16)) return launch_gemm_i8(p, pair, stream);
+        if (pair) pick<true, 0>(p, ngroups, slots, mean, s);
+        else pick<false, 0>(p, ngroups, slots, mean, s);
     }
     MOEQ_CHECK_LAUNCH();
     return MOE_OK;

@@ -236,6 +236,10 @@ struct I8Pass {
     const int8_t* q;
     int64_t ldq;
     const float* qscale;
+    const void* x;               // != NULL: uncoded rows of x_dtype, ldx apart, in
+    int64_t ldx;                 // place of q, which the kernel codes itself
+    int32_t x_dtype;             // (i8_codes_itself)
+    bool x_vec8;                 // K % 8 == 0 and rows 16-byte aligned
     const int32_t* offsets;
     const int32_t* perm_src;
     int64_t T;
@@ -244,6 +248,9 @@ struct I8Pass {
     int64_t ld_out;
     int32_t out_dtype;
 };
+// Whether the pass takes uncoded rows: few enough of them (measured below the
+// launch that coding them apart costs), and their codes fit a workgroup's LDS.
+bool i8_codes_itself(int64_t T, int32_t k, int32_t K, bool routed);
 int launch_i8(const I8Pass& p, bool pair, void* stream);
 int launch_gemm_i8(const I8Pass& p, bool pair, void* stream);
 int launch_probe_read(const void* buf, size_t bytes, uint32_t* sink, int blocks, void* stream);

@@ -285,7 +285,7 @@ def test_row_checks():
     assert mb._rows(t, "t", 4, 10, dev) == 10
     assert mb._rows(t[:, 2:8], "t", 4, 6, dev) == 10
     assert mb._rows(t[::2], "t", 2, 10, dev) == 20
-    assert mb._rows(t[:1, :3], "t", 1, 3, dev) == 10
+    assert mb._rows(t[:1, :3], "t", 1, 3, dev) == 3
     for bad in (t.t(), t[:, ::2], t[0]):
         with pytest.raises(ValueError):
             mb._rows(bad, "t", bad.shape[0], bad.shape[-1], dev)

@@ -134,6 +134,28 @@ def test_linear(T, K, N, dt):
     assert torch.equal(out2, out)
 
 
+# one case for every kernel that the number of tiles picks: the streaming kernel
+# over 1, 4 and 8 input parts, and each GEMM tile
+@pytest.mark.parametrize("T,K,N", [(3, 700, 16400), (9, 200, 16400), (4, 333, 4200), (16, 1300, 4112),
+                                   (1, 72, 16390), (1300, 192, 4096), (640, 136, 4090),
+                                   (640, 328, 2048), (30, 264, 41000), (50, 200, 16384),
+                                   (200, 520, 1040), (4, 6144, 100), (4, 6145, 100),
+                                   (1, 24576, 33), (1, 24640, 33), (3, 8192, 33)])
+def test_linear_every_kernel(T, K, N):
+    say("linear kernels", T, K, N)
+    rs = np.random.default_rng(T + K + N)
+    W, S = codes(rs, (N, K)), scales(rs, N)
+    lin = moeq.I8Linear(W, S)
+    for dt in ("bf16", "fp32"):
+        x = rnd(rs, (T, K), TYPES[dt], 2.0)
+        out = moeq.linear_i8(lin, x)
+        q, s = moeq.quantize_i8(x)
+        check_linear(lin, W.cpu().numpy(), f64(S), None, q.cpu().numpy()[:, :K], s.cpu().numpy(),
+                     out, (T, K, N, dt))
+        # rows coded inside the product: the bits of coding them apart
+        assert torch.equal(moeq.linear_i8(lin, q, s, out_dtype=x.dtype), out)
+
+
 def test_linear_strided_in_and_out():
     rs = np.random.default_rng(4)
     T, K, N = 37, 96, 80
@@ -224,7 +246,9 @@ def run_experts(T, E, k, H, I, x_t, y_t, seed, ids=None):
                                        (5, 3, 2, 100, 33), (17, 8, 3, 1, 1), (37, 16, 4, 272, 80),
                                        (64, 4, 2, 128, 320), (130, 8, 8, 320, 64),
                                        (200, 70, 5, 192, 48), (300, 4, 1, 144, 112),
-                                       (600, 2, 2, 192, 96)])
+                                       (600, 2, 2, 192, 96), (90, 40, 8, 72, 528),
+                                       (260, 40, 8, 72, 520), (700, 40, 8, 72, 264),
+                                       (4, 40, 4, 1000, 200), (2, 130, 8, 72, 136)])
 @pytest.mark.parametrize("x_t,y_t", [("bf16", "bf16"), ("fp32", "fp32"), ("fp16", "fp16")])
 def test_expert_ffn(T, E, k, H, I, x_t, y_t):
     say("expert_ffn", T, E, k, H, I, x_t)
@@ -240,6 +264,8 @@ def test_expert_ffn_one_expert_takes_all_and_repeated_ids():
     run_experts(T, E, k, 128, 64, "bf16", "fp32", 1, ids)
     ids[:, 1] = 63
     run_experts(T, E, k, 128, 64, "bf16", "fp32", 2, ids)
+    # few rows, coded inside the products one at a time
+    run_experts(8, 3, 2, 136, 72, "bf16", "fp32", 3, np.full((8, 2), 1))
 
 
 @pytest.mark.parametrize("T,H,I", [(1, 256, 128), (3, 100, 40), (16, 272, 80), (33, 64, 200),
