@@ -76,7 +76,7 @@ int take_rows(I8Pass& p, const void* x, int dt, int64_t ldx, const float* x_scal
         p.qscale = x_scale;
         return MOE_OK;
     }
-    if (i8_codes_itself(p.T, p.k, p.K, p.offsets != nullptr)) {
+    if (i8_codes_itself(p.T, p.K, p.offsets != nullptr)) {
         p.x = x;
         p.ldx = ldx;
         p.x_dtype = dt;

@@ -11,7 +11,8 @@
 //
 // A workgroup owns a row and keeps it in registers (NCH chunks of V elements
 // per thread), so every operand is read once and every result written once;
-// the reductions (b^2, r'^2, max |n|) go through LDS.
+// the reductions (b^2, r'^2, max |n|) go through LDS.  HBM bounds many rows,
+// the latency of a launch and of two or three dependent steps few.
 #include "elem_dev.h"
 
 namespace moeq {
@@ -30,7 +31,8 @@ template <int V, int NCH, int COMB>
 __global__ __launch_bounds__(1024) void k_block(BlockRow A) {
     constexpr bool EARLY = V * NCH <= 8;
     constexpr int NE = EARLY ? NCH : 1;
-    __shared__ float red[3][16];
+    __shared__ float red[2][V == 8 ? 64 : 512];
+    __shared__ uint32_t red_max[16];
     const moe_block& b = A.b;
     const int64_t t = blockIdx.x;
     const int H = A.H, nt = A.nw * 64;
@@ -115,15 +117,28 @@ __global__ __launch_bounds__(1024) void k_block(BlockRow A) {
     }
 
     // ------------------------------------------------ the norm after
-    auto norm = [&](float* r) {
-        float ss = 0.f;
+    // The sum of squares: by chunk, then 64 neighbouring chunks over lanes, then
+    // these in order, whatever part of the row a wave holds.
+    auto norm = [&](float* part) {
+        const int n64 = (H + 64 * V - 1) / (64 * V);
+        float total = 0.f;
 #pragma unroll
-        for (int c = 0; c < NCH; ++c)
+        for (int c = 0; c < NCH; ++c) {
+            float ss = 0.f;
             if (place(c) < H)
 #pragma unroll
                 for (int e = 0; e < V; ++e) ss += v[c][e] * v[c][e];
-        ss = block_sum(ss, r, A.nw);
-        return 1.f / sqrtf(ss / (float)H + b.eps);
+            ss = wave_sum(ss);
+            if (c == 0) total = ss;          // the whole row where it is one such part
+            const int i = c * A.nw + ((int)threadIdx.x >> 6);
+            if (n64 > 1 && i < n64 && (threadIdx.x & 63) == 0) part[i] = ss;
+        }
+        if (n64 > 1) {
+            __syncthreads();
+            total = 0.f;
+            for (int i = 0; i < n64; ++i) total += part[i];
+        }
+        return 1.f / sqrtf(total / (float)H + b.eps);
     };
     float rstd = 1.f;
     if (has_y && b.post_w) rstd = norm(red[0]);
@@ -187,7 +202,7 @@ __global__ __launch_bounds__(1024) void k_block(BlockRow A) {
     if (!b.q_out) return;
 
     // ------------------------------------------------ its 8-bit code
-    amax = block_max(amax, reinterpret_cast<uint32_t*>(red[2]), A.nw);
+    amax = block_max(amax, red_max, A.nw);
     const RowCode rc = row_code(amax);
     if (threadIdx.x == 0) b.q_scale[t] = rc.scale;
     int8_t* q = b.q_out + t * b.ld_q;
@@ -209,7 +224,7 @@ __global__ __launch_bounds__(1024) void k_block(BlockRow A) {
 
 template <int V, int NCH>
 void launch(const BlockRow& A, int64_t T, hipStream_t s) {
-    constexpr int C = V == 1 && NCH > 8 ? 2 : 4;
+    constexpr int C = V == 1 && NCH > 8 ? 1 : 4;
     if (A.b.k > 0)
         k_block<V, NCH, C><<<(unsigned)T, A.nw * 64, 0, s>>>(A);
     else
@@ -225,12 +240,18 @@ int launch_block(const moe_block& b, int64_t T, int32_t H, bool vec8, void* stre
     const int nch = (H + V - 1) / V;
     BlockRow A{b, H, 1};
     auto waves = [&](int per) { return (nch + 64 * per - 1) / (64 * per); };
+    // Few rows: as many threads as a row has chunks (one token, H 6144: 3.2 us
+    // with one chunk a thread, 4.0 with two).  Many rows of 16-bit types: two
+    // (4096 x 6144, norm after and before: 39.2 us against 43.0; fp32 rows lose,
+    // 85.6 against 78.9).  The bits are the same.
+    const bool many = T >= 1024 && b.r_dtype != MOE_DT_F32 && b.y_dtype != MOE_DT_F32;
     if (vec8) {
-        if (waves(1) <= 16) { A.nw = waves(1); launch<8, 1>(A, T, s); }
+        if (waves(1) <= 16 && !(many && nch > 512)) { A.nw = waves(1); launch<8, 1>(A, T, s); }
         else if (waves(2) <= 16) { A.nw = waves(2); launch<8, 2>(A, T, s); }
         else { A.nw = waves(4); launch<8, 4>(A, T, s); }
     } else {
-        if (waves(8) <= 16) { A.nw = waves(8); launch<1, 8>(A, T, s); }
+        if (waves(2) <= 16 && T < 1024) { A.nw = waves(2); launch<1, 2>(A, T, s); }
+        else if (waves(4) <= 16) { A.nw = waves(4); launch<1, 4>(A, T, s); }
         else { A.nw = waves(32); launch<1, 32>(A, T, s); }
     }
     MOEQ_CHECK_LAUNCH();

@@ -248,9 +248,9 @@ struct I8Pass {
     int64_t ld_out;
     int32_t out_dtype;
 };
-// Whether the pass takes uncoded rows: few enough of them (measured below the
-// launch that coding them apart costs), and their codes fit a workgroup's LDS.
-bool i8_codes_itself(int64_t T, int32_t k, int32_t K, bool routed);
+// Whether the pass takes uncoded rows: one matrix, few rows, and their codes
+// fit a workgroup's LDS.
+bool i8_codes_itself(int64_t T, int32_t K, bool routed);
 int launch_i8(const I8Pass& p, bool pair, void* stream);
 int launch_gemm_i8(const I8Pass& p, bool pair, void* stream);
 int launch_probe_read(const void* buf, size_t bytes, uint32_t* sink, int blocks, void* stream);

@@ -18,8 +18,7 @@ struct QuantArgs {
     int64_t ldx, ldq, T;
     int8_t* q;
     float* scale;
-    int dt, K, nw;   // nw: waves per row
-    int rows;        // rows per workgroup (one wave each when > 1)
+    int dt, K, nw;   // nw: waves of a row
 };
 
 template <int V>
@@ -36,10 +35,8 @@ __device__ __forceinline__ void store_codes(int8_t* q, int h, const float (&v)[V
 template <int V, int NCH>
 __global__ __launch_bounds__(1024) void k_quantize(QuantArgs A) {
     __shared__ uint32_t red[16];
-    const int tid = A.rows > 1 ? threadIdx.x & 63 : threadIdx.x;
-    const int nt = A.nw * 64;
-    const int64_t t = (int64_t)blockIdx.x * A.rows + (A.rows > 1 ? threadIdx.x >> 6 : 0);
-    if (t >= A.T) return;   // whole waves, and only where a row is one wave
+    const int tid = threadIdx.x, nt = A.nw * 64;
+    const int64_t t = blockIdx.x;
     int8_t* q = A.q + t * A.ldq;
     uint32_t amax = 0u;
     if constexpr (NCH > 0) {
@@ -116,12 +113,11 @@ void launch_q(QuantArgs A, hipStream_t s) {
     auto go = [&](auto tag, int per) {
         constexpr int NCH = decltype(tag)::value;
         A.nw = per ? waves(per) : 16;
-        A.rows = 1;
         k_quantize<V, NCH><<<(unsigned)A.T, A.nw * 64, 0, s>>>(A);
     };
-    constexpr int C = V == 8 ? 1 : 8;
-    if (waves(C) <= 16) go(std::integral_constant<int, C>{}, C);
-    else if (waves(4 * C) <= 16) go(std::integral_constant<int, 4 * C>{}, 4 * C);
+    constexpr int C0 = V == 8 ? 1 : 2, C1 = V == 8 ? 4 : 16;
+    if (waves(C0) <= 16) go(std::integral_constant<int, C0>{}, C0);
+    else if (waves(C1) <= 16) go(std::integral_constant<int, C1>{}, C1);
     else go(std::integral_constant<int, 0>{}, 0);
 }
 
@@ -130,7 +126,7 @@ void launch_q(QuantArgs A, hipStream_t s) {
 int launch_quantize_i8(const void* x, int dt, int64_t ldx, int64_t T, int32_t K, int8_t* q,
                        int64_t ldq, float* scale, bool vec8, void* stream) {
     hipStream_t s = reinterpret_cast<hipStream_t>(stream);
-    QuantArgs A{x, ldx, ldq, T, q, scale, dt, K, 1, 1};
+    QuantArgs A{x, ldx, ldq, T, q, scale, dt, K, 1};
     if (vec8) launch_q<8>(A, s);
     else launch_q<1>(A, s);
     MOEQ_CHECK_LAUNCH();

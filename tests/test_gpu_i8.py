@@ -264,7 +264,7 @@ def test_expert_ffn_one_expert_takes_all_and_repeated_ids():
     run_experts(T, E, k, 128, 64, "bf16", "fp32", 1, ids)
     ids[:, 1] = 63
     run_experts(T, E, k, 128, 64, "bf16", "fp32", 2, ids)
-    # few rows, coded inside the products one at a time
+    # few rows, all on one expert
     run_experts(8, 3, 2, 136, 72, "bf16", "fp32", 3, np.full((8, 2), 1))
 
 
