@@ -137,14 +137,15 @@ def _bind(L):
 def _call(name, dev, *args):
     """One library call on dev and its current stream."""
     L = lib()
-    if _fns.get("lib") is not L:
+    f = _fns
+    if f.get("lib") is not L:
         _bind(L)
     i = dev.index
-    if i == _fns["device"]():
-        st = _fns[name](*args, _fns["stream"](i))
+    if i == f["device"]():
+        st = f[name](*args, f["stream"](i))
     else:
         with _torch().cuda.device(dev):
-            st = _fns[name](*args, _fns["stream"](i))
+            st = f[name](*args, f["stream"](i))
     if st != MOE_OK:
         _check(st, name)
 
@@ -180,9 +181,8 @@ def _vector(t, name, H, dev, dtype=None):
     return t.data_ptr()
 
 
-def _block(dev, T, H, r, y, w, k=0, inv_perm=None, topk_w=None, y_shared=None, shared_gate=None,
-           post_w=None, gate=None, y_scale=1.0, r_scale=1.0, eps=1e-5, w_offset=0.0, r_out=None,
-           out=None, out_dtype=None, codes=False, q=None, scale=None):
+def _block(dev, T, H, r, y, w, k, inv_perm, topk_w, y_shared, shared_gate, post_w, gate, y_scale,
+           r_scale, eps, w_offset, r_out, out, out_dtype, codes, q, scale):
     torch = _torch()
     y_p = y_ld = y_t = inv_p = tw_p = ys_p = ys_ld = ys_t = sg_p = 0
     w_p = pw_p = w_t = g_p = g_ld = g_lh = g_t = 0
@@ -243,8 +243,8 @@ def block_norm(r, w, *, eps=1e-5, w_offset=0.0, out=None, out_dtype=None, codes=
     itself unwritten (returned as None)."""
     dev = _cuda(r, "block_norm")
     T, H = r.shape
-    n, q, scale = _block(dev, T, H, r, None, w, eps=eps, w_offset=w_offset, out=out,
-                         out_dtype=out_dtype, codes=codes, q=q, scale=scale)
+    n, q, scale = _block(dev, T, H, r, None, w, 0, None, None, None, None, None, None, 1.0, 1.0,
+                         eps, w_offset, None, out, out_dtype, codes, q, scale)
     return (n, q, scale) if codes else n
 
 
@@ -262,9 +262,8 @@ def block_residual(r, y, w=None, *, post_w=None, gate=None, y_scale=1.0, r_scale
     T, H = r.shape
     if r_out is None:
         r_out = torch.empty((T, H), dtype=r.dtype, device=dev)
-    n, q, scale = _block(dev, T, H, r, y, w, post_w=post_w, gate=gate, y_scale=y_scale,
-                         r_scale=r_scale, eps=eps, w_offset=w_offset, r_out=r_out, out=out,
-                         out_dtype=out_dtype, codes=codes, q=q, scale=scale)
+    n, q, scale = _block(dev, T, H, r, y, w, 0, None, None, None, None, post_w, gate, y_scale,
+                         r_scale, eps, w_offset, r_out, out, out_dtype, codes, q, scale)
     return (r_out, n, q, scale) if codes else (r_out, n)
 
 
@@ -284,10 +283,9 @@ def combine_residual(r, y_perm, inv_perm, topk_w, w=None, *, y_shared=None, shar
         r_out = torch.empty((T, H), dtype=torch.float32 if r is None else r.dtype, device=dev)
     if shared_gate is not None and y_shared is None:
         raise ValueError("shared_gate needs y_shared")
-    n, q, scale = _block(dev, T, H, r, y_perm, w, k=k, inv_perm=inv_perm, topk_w=topk_w,
-                         y_shared=y_shared, shared_gate=shared_gate, post_w=post_w, gate=gate,
-                         y_scale=y_scale, r_scale=r_scale, eps=eps, w_offset=w_offset,
-                         r_out=r_out, out=out, out_dtype=out_dtype, codes=codes, q=q, scale=scale)
+    n, q, scale = _block(dev, T, H, r, y_perm, w, k, inv_perm, topk_w, y_shared, shared_gate,
+                         post_w, gate, y_scale, r_scale, eps, w_offset, r_out, out, out_dtype,
+                         codes, q, scale)
     return (r_out, n, q, scale) if codes else (r_out, n)
 
 

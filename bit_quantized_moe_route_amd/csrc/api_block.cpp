@@ -45,6 +45,15 @@ int check_codes(const std::string& fn, const char* name, const void* q, int64_t 
     return MOE_OK;
 }
 
+// The products' workgroups: at most rows / 128 + E tiles of rows (smaller tiles
+// are for fewer rows) by N / 256 of channels, in one launch of less than 2^31.
+int check_tiles(const std::string& fn, int64_t rows, int64_t E, int64_t N) {
+    const int64_t bm = rows > (int64_t)1 << 20 ? 128 : 32;
+    if ((rows / bm + E + 1) * (N / 64 + 1) >= kMaxRows - 4096)
+        return fail(MOE_EUNSUPPORTED, fn + ": too many rows and channels for one call");
+    return MOE_OK;
+}
+
 // x as the product calls take it: codes with a scale per row, or rows of a
 // float type that the call quantises into its workspace.
 int check_x(const std::string& fn, const void* x, int dt, int64_t ldx, const float* x_scale,
@@ -143,6 +152,8 @@ int run_ffn_i8(const std::string& fn, const moe_i8_layer* L, const void* x, int3
     if (!aligned(y, (uintptr_t)dt_bytes(y_dtype))) return bad(fn, "the output is misaligned");
     bool vec8 = false;
     int st = check_x(fn, x, x_dtype, ldx, x_scale, L->H, vec8);
+    if (st) return st;
+    st = check_tiles(fn, T * k, L->E, 2 * (int64_t)(L->H > L->I ? L->H : L->I));
     if (st) return st;
     const FfnWs lay = ffn_i8_ws(L, T, k);
     if (!ws || ws_bytes < lay.total)
@@ -310,6 +321,8 @@ int moe_linear_i8(const moe_i8_linear* linear, const void* x, int32_t x_dtype, i
     if (ldo < linear->N) return bad(fn, "the row stride of out is below N");
     bool vec8 = false;
     st = check_x(fn, x, x_dtype, ldx, x_scale, linear->K, vec8);
+    if (st) return st;
+    st = check_tiles(fn, T, 1, linear->N);
     if (st) return st;
     if (x_dtype != MOE_DT_I8) {
         const size_t need = codes_ws(T, linear->K);

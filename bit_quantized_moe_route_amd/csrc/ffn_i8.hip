@@ -30,19 +30,21 @@ struct Rows {
 __device__ __forceinline__ Rows find_rows(const I8Pass& A, int s, int lane) {
     if (!A.offsets) return Rows{0, 0, A.T};
     int seen = 0;
-    for (int e0 = 0; e0 < A.E; e0 += 64) {
-        const int e = e0 + lane;
-        const int o0 = e < A.E ? A.offsets[e] : 0;
-        const int o1 = e < A.E ? A.offsets[e + 1] : 0;
-        uint64_t m = __ballot(o1 > o0);
-        const int n = __popcll(m);
-        if (s < seen + n) {
-            for (int i = 0; i < s - seen; ++i) m &= m - 1;
-            const int owner = __ffsll((unsigned long long)m) - 1;
-            const int a = __shfl(o0, owner), b = __shfl(o1, owner);
-            return Rows{uniform(e0 + owner), uniform(a), uniform(b - a)};
+    for (int e0 = 0; e0 < A.E; e0 += 256) {
+        const Offsets4 o = load_offsets(A.offsets, A.E, e0, lane);
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+            uint64_t m = __ballot(o.o1[c] > o.o0[c]);
+            const int n = __popcll(m);
+            if (s < seen + n) {
+                for (int i = 0; i < s - seen; ++i) m &= m - 1;
+                const int owner = uniform(__ffsll((unsigned long long)m) - 1);
+                const int a = __builtin_amdgcn_readlane(o.o0[c], owner);
+                return Rows{e0 + 64 * c + owner, a,
+                            __builtin_amdgcn_readlane(o.o1[c], owner) - a};
+            }
+            seen += n;
         }
-        seen += n;
     }
     return Rows{-1, 0, 0};
 }

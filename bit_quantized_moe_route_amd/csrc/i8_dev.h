@@ -25,6 +25,25 @@ __device__ __forceinline__ void keep_order() {
 // around matrix instructions go by, which run whatever the lane mask says.
 __device__ __forceinline__ int uniform(int v) { return __builtin_amdgcn_readfirstlane(v); }
 
-__device__ __forceinline__ float silu_mul(float g, float u) { return g / (1.f + __expf(-g)) * u; }
+// silu(g) * u.  The exponential and the reciprocal are the hardware's (each
+// within an ulp or two of fp32), far inside what the 8-bit code of h resolves.
+__device__ __forceinline__ float silu_mul(float g, float u) {
+    return g * __builtin_amdgcn_rcpf(1.f + __expf(-g)) * u;
+}
+
+// Offsets of experts e0 + 64 c + lane, c < 4, all loads in flight together.
+struct Offsets4 {
+    int o0[4], o1[4];
+};
+__device__ __forceinline__ Offsets4 load_offsets(const int32_t* offsets, int E, int e0, int lane) {
+    Offsets4 o;
+#pragma unroll
+    for (int c = 0; c < 4; ++c) {
+        const int e = e0 + 64 * c + lane;
+        o.o0[c] = e < E ? offsets[e] : 0;
+        o.o1[c] = e < E ? offsets[e + 1] : 0;
+    }
+    return o;
+}
 
 }  // namespace moeq

@@ -210,6 +210,7 @@ def lin(**kw):
     ({}, (P, 2, 64, None, 1, P, 2, 32, None, 0), moeq.MOE_EWORKSPACE),
     ({}, (P, 2, 64, None, 1, P, 2, 32, P, 64), moeq.MOE_EWORKSPACE),
     ({}, (P, 2, 64, None, 1, P, 2, 32, P + 16, 1 << 20), moeq.MOE_EINVAL),
+    (dict(N=1 << 24), (P, 4, 64, P, 1 << 24, P, 2, 1 << 24, None, 0), moeq.MOE_EUNSUPPORTED),
 ])
 def test_linear_refusals(desc, args, status):
     refused("moe_linear_i8", lin(**desc), *args, None, status=status)

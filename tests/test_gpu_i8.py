@@ -310,6 +310,8 @@ def test_empty_batches():
     x = torch.empty((0, 64), dtype=torch.bfloat16, device=DEV)
     assert moeq.linear_i8(lin, x).shape == (0, 48)
     assert moeq.shared_ffn_i8(layer, x).shape == (0, 64)
+    r = moeq.forward_i8(layer, x, torch.empty((0, 1), device=DEV), 1, shared=layer)
+    assert r["out"].shape == (0, 64) and r["counts"].tolist() == [0]
     q, s = moeq.quantize_i8(x)
     assert q.shape == (0, 64) and s.shape == (0,)
 
@@ -371,6 +373,75 @@ def test_block_of_a_decoder():
                 assert torch.equal(now[name][:, :H], held[name][:, :H])
             else:
                 assert torch.equal(now[name], held[name]), (i, name)
+
+
+def test_codes_or_float_rows_from_slices():
+    """A layer fed from columns of a wider tensor, and from code rows that lie
+    further apart."""
+    rs = np.random.default_rng(17)
+    layer, _ = make_layer(rs, 1, 96, 48)
+    for T in (3, 30):
+        wide = rnd(rs, (T, 300), torch.bfloat16)
+        for a in (0, 5):
+            x = wide[:, a:a + 96]
+            ref = moeq.shared_ffn_i8(layer, x.contiguous())
+            assert torch.equal(moeq.shared_ffn_i8(layer, x), ref)
+            q, s = moeq.quantize_i8(x)
+            big = torch.full((T, 512), 99, dtype=torch.int8, device=DEV)
+            big[:, 64:64 + 128] = q
+            assert torch.equal(moeq.shared_ffn_i8(layer, big[:, 64:64 + 128], s, y_dtype=x.dtype), ref)
+
+
+def test_refusals_of_shapes():
+    rs = np.random.default_rng(18)
+    layer, _ = make_layer(rs, 4, 96, 48)
+    lin = moeq.I8Linear(codes(rs, (48, 96)), scales(rs, 48))
+    x = rnd(rs, (5, 96), torch.bfloat16)
+    q, s = moeq.quantize_i8(x)
+    ids = torch.zeros((5, 1), dtype=torch.int32, device=DEV)
+    _, off, perm, _ = moeq.permute(ids, 4)
+    for call in (lambda: moeq.linear_i8(lin, x[:, :95]), lambda: moeq.linear_i8(lin, x.t()),
+                 lambda: moeq.linear_i8(lin, x.double()), lambda: moeq.linear_i8(lin, q),
+                 lambda: moeq.linear_i8(lin, x, s), lambda: moeq.linear_i8(lin, q[:, :96], s),
+                 lambda: moeq.linear_i8(lin, q, s[:4]),
+                 lambda: moeq.linear_i8(lin, x, out=torch.empty((5, 47), device=DEV)),
+                 lambda: moeq.linear_i8(lin, x, out=torch.empty((5, 48))),
+                 lambda: moeq.linear_i8(lin, x, ws=torch.empty(9999)),
+                 lambda: moeq.expert_ffn_i8(layer, x, perm, off[:4], 1),
+                 lambda: moeq.expert_ffn_i8(layer, x, perm.long(), off, 1),
+                 lambda: moeq.expert_ffn_i8(layer, x, perm, off, 2),
+                 lambda: moeq.expert_ffn_i8(layer, x.cpu(), perm, off, 1),
+                 lambda: moeq.block_norm(x, torch.ones(95, device=DEV)),
+                 lambda: moeq.block_norm(x, torch.ones(96)),
+                 lambda: moeq.block_residual(x, x[:4], None),
+                 lambda: moeq.block_residual(x, x, torch.ones(96, device=DEV), post_w=x[0]),
+                 lambda: moeq.block_residual(x, x, None, gate=torch.ones((3, 1), device=DEV)),
+                 lambda: moeq.block_residual(x, x, None, gate=torch.ones(96, device=DEV)),
+                 lambda: moeq.block_residual(x, x, None, r_out=x.float()),
+                 lambda: moeq.block_norm(x, x[0], codes=True, q=q[:, :96]),
+                 lambda: moeq.I8Linear(codes(rs, (48, 96)), scales(rs, 47)),
+                 lambda: moeq.I8Layer(codes(rs, (2, 96, 64)), scales(rs, (2, 96)),
+                                      codes(rs, (2, 64, 47)), scales(rs, (2, 64)))):
+        with pytest.raises(ValueError):
+            call()
+    for call in (lambda: moeq.shared_ffn_i8(layer, x),
+                 lambda: moeq.linear_i8(lin, x, ws=torch.empty(8, dtype=torch.uint8, device=DEV)),
+                 lambda: moeq.block_norm(x, None)):
+        with pytest.raises(moeq.MoeError):
+            call()
+
+
+def test_gated_sum_is_combine():
+    """combine_residual without a residual stream gives the bits of combine and
+    combine_shared on fp32 rows."""
+    T, k, H, E = 13, 4, 200, 8
+    rs = np.random.default_rng(19)
+    logits = torch.from_numpy(rs.standard_normal((T, E)).astype(np.float32)).to(DEV)
+    _, tw, _, _, _, inv = moeq.route_permute(logits, k)
+    y, ys = rnd(rs, (T * k, H), torch.float32), rnd(rs, (T, H), torch.float32)
+    assert torch.equal(moeq.combine_residual(None, y, inv, tw)[0], moeq.combine(y, inv, tw))
+    assert torch.equal(moeq.combine_residual(None, y, inv, tw, y_shared=ys)[0],
+                       moeq.combine_shared(y, inv, tw, ys))
 
 
 def test_side_stream():
