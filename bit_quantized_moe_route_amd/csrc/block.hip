@@ -13,6 +13,8 @@
 // per thread), so every operand is read once and every result written once;
 // the reductions (b^2, r'^2, max |n|) go through LDS.  HBM bounds many rows,
 // the latency of a launch and of two or three dependent steps few.
+#include <type_traits>
+
 #include "elem_dev.h"
 
 namespace moeq {
@@ -21,13 +23,14 @@ namespace {
 
 struct BlockRow {
     moe_block b;
-    int H, nw;
+    int H, nw;      // nw: waves of a row
 };
 
 // COMB: slots of the gated sum that are in flight together, 0: y is a row.
-// Everything the row needs is loaded before the first reduction (EARLY), while
+// STREAM: more rows than the caches hold; results (1) and the rows of a gated
+// sum (2) go past them.  Everything the row needs is loaded before the first reduction (EARLY), while
 // it fits the registers of a workgroup of 1024 threads.
-template <int V, int NCH, int COMB>
+template <int V, int NCH, int COMB, int STREAM>
 __global__ __launch_bounds__(1024) void k_block(BlockRow A) {
     constexpr bool EARLY = V * NCH <= 8;
     constexpr int NE = EARLY ? NCH : 1;
@@ -90,7 +93,7 @@ __global__ __launch_bounds__(1024) void k_block(BlockRow A) {
             for (int c = 0; c < NCH; ++c) {
                 Raw<V> y[COMB];
 #pragma unroll
-                for (int u = 0; u < COMB; ++u) y[u].load(b.y, b.y_dtype, row[u] + at(c));
+                for (int u = 0; u < COMB; ++u) y[u].template load<STREAM == 2>(b.y, b.y_dtype, row[u] + at(c));
 #pragma unroll
                 for (int u = 0; u < COMB; ++u) {
                     if (j0 + u >= b.k) break;
@@ -177,7 +180,8 @@ __global__ __launch_bounds__(1024) void k_block(BlockRow A) {
             for (int e = 0; e < V; ++e)
                 v[c][e] = has_y ? b.r_scale * f[e] + v[c][e] : b.r_scale * f[e];
         }
-        if (b.r_out && place(c) < H) store_f32<V>(b.r_out, b.r_dtype, t * b.ld_r_out + place(c), v[c]);
+        if (b.r_out && place(c) < H)
+            store_f32<V, (STREAM > 0)>(b.r_out, b.r_dtype, t * b.ld_r_out + place(c), v[c]);
     }
     if (!b.n_out && !b.q_out) return;
 
@@ -195,7 +199,7 @@ __global__ __launch_bounds__(1024) void k_block(BlockRow A) {
             for (int e = 0; e < V; ++e) v[c][e] = v[c][e] * rstd * (b.w_offset + f[e]);
         }
         if (place(c) >= H) continue;
-        if (b.n_out) store_f32<V>(b.n_out, b.n_dtype, t * b.ld_n + place(c), v[c]);
+        if (b.n_out) store_f32<V, (STREAM > 0)>(b.n_out, b.n_dtype, t * b.ld_n + place(c), v[c]);
 #pragma unroll
         for (int e = 0; e < V; ++e) amax = max(amax, __float_as_uint(v[c][e]) & 0x7fffffffu);
     }
@@ -225,10 +229,20 @@ __global__ __launch_bounds__(1024) void k_block(BlockRow A) {
 template <int V, int NCH>
 void launch(const BlockRow& A, int64_t T, hipStream_t s) {
     constexpr int C = V == 1 && NCH > 8 ? 1 : 4;
-    if (A.b.k > 0)
-        k_block<V, NCH, C><<<(unsigned)T, A.nw * 64, 0, s>>>(A);
-    else
-        k_block<V, NCH, 0><<<(unsigned)T, A.nw * 64, 0, s>>>(A);
+    // Results of 2M elements and more go past the caches (4096 rows of 6144 bf16
+    // that were not in them: 26.2 -> 23.0 us for the norm alone, 116 -> 103 with
+    // the gated sum of 8 rows each, which are then read past them too; fp32
+    // rows are not: 194 us against 181).
+    const bool stream = V == 8 && T * A.H >= (int64_t)1 << 21;
+    auto go = [&](auto comb) {
+        constexpr int K = decltype(comb)::value;
+        constexpr int S1 = V == 8 ? 1 : 0, S2 = V == 8 && K ? 2 : S1;
+        if (!stream) k_block<V, NCH, K, 0><<<(unsigned)T, A.nw * 64, 0, s>>>(A);
+        else if (A.b.y_dtype == MOE_DT_F32) k_block<V, NCH, K, S1><<<(unsigned)T, A.nw * 64, 0, s>>>(A);
+        else k_block<V, NCH, K, S2><<<(unsigned)T, A.nw * 64, 0, s>>>(A);
+    };
+    if (A.b.k > 0) go(std::integral_constant<int, C>{});
+    else go(std::integral_constant<int, 0>{});
 }
 
 }  // namespace
@@ -240,13 +254,13 @@ int launch_block(const moe_block& b, int64_t T, int32_t H, bool vec8, void* stre
     const int nch = (H + V - 1) / V;
     BlockRow A{b, H, 1};
     auto waves = [&](int per) { return (nch + 64 * per - 1) / (64 * per); };
-    // Few rows: as many threads as a row has chunks (one token, H 6144: 3.2 us
-    // with one chunk a thread, 4.0 with two).  Many rows of 16-bit types: two
-    // (4096 x 6144, norm after and before: 39.2 us against 43.0; fp32 rows lose,
-    // 85.6 against 78.9).  The bits are the same.
-    const bool many = T >= 1024 && b.r_dtype != MOE_DT_F32 && b.y_dtype != MOE_DT_F32;
+    // As many threads as a row has chunks, up to 1024 (one token, H 6144: 3.2 us
+    // against 4.0 with two chunks a thread; 4096 tokens from HBM, norm after and
+    // before: 50 against 54).  Rows off 16 bytes: two elements a thread for few
+    // rows, four for many (333 / 4096 rows of 1003 fp32: 5.2 / 14.2 us with two,
+    // 6.1 / 11.8 with four).  The bits are the same.
     if (vec8) {
-        if (waves(1) <= 16 && !(many && nch > 512)) { A.nw = waves(1); launch<8, 1>(A, T, s); }
+        if (waves(1) <= 16) { A.nw = waves(1); launch<8, 1>(A, T, s); }
         else if (waves(2) <= 16) { A.nw = waves(2); launch<8, 2>(A, T, s); }
         else { A.nw = waves(4); launch<8, 4>(A, T, s); }
     } else {

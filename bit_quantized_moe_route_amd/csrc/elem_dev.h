@@ -15,14 +15,21 @@ struct Raw8 {
     u32x4 a, b;
 };
 
+template <bool STREAM = false>
+__device__ __forceinline__ u32x4 load16(const u32x4* q) {
+    if constexpr (STREAM) return __builtin_nontemporal_load(q);
+    return *q;
+}
+
+template <bool STREAM = false>
 __device__ __forceinline__ Raw8 load_raw8(const void* p, int dt, int64_t i) {
     Raw8 r;
     if (dt == MOE_DT_F32) {
         const u32x4* q = reinterpret_cast<const u32x4*>(static_cast<const float*>(p) + i);
-        r.a = q[0];
-        r.b = q[1];
+        r.a = load16<STREAM>(q);
+        r.b = load16<STREAM>(q + 1);
     } else {
-        r.a = *reinterpret_cast<const u32x4*>(static_cast<const uint16_t*>(p) + i);
+        r.a = load16<STREAM>(reinterpret_cast<const u32x4*>(static_cast<const uint16_t*>(p) + i));
         r.b = u32x4{0u, 0u, 0u, 0u};
     }
     return r;
@@ -61,14 +68,16 @@ struct Raw;
 template <>
 struct Raw<8> {
     Raw8 r;
+    template <bool STREAM = false>
     __device__ __forceinline__ void load(const void* p, int dt, int64_t i) {
-        r = load_raw8(p, dt, i);
+        r = load_raw8<STREAM>(p, dt, i);
     }
     __device__ __forceinline__ void f32(int dt, float (&v)[8]) const { raw_to_f32(r, dt, v); }
 };
 template <>
 struct Raw<1> {
     uint32_t r;
+    template <bool STREAM = false>
     __device__ __forceinline__ void load(const void* p, int dt, int64_t i) {
         r = dt == MOE_DT_F32 ? static_cast<const uint32_t*>(p)[i]
                              : static_cast<const uint16_t*>(p)[i];
@@ -100,21 +109,30 @@ __device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
     return __builtin_bit_cast(uint32_t, f16x2{(_Float16)lo, (_Float16)hi});
 }
 
-// One rounding to the stored type, nearest even.
-template <int V>
+// One rounding to the stored type, nearest even.  STREAM: results that no
+// cache will hold until they are read (8 elements at a time only).
+template <int V, bool STREAM = false>
 __device__ __forceinline__ void store_f32(void* p, int dt, int64_t i, const float (&v)[V]) {
     if constexpr (V == 8) {
         if (dt == MOE_DT_F32) {
             f32x4* q = reinterpret_cast<f32x4*>(static_cast<float*>(p) + i);
-            q[0] = f32x4{v[0], v[1], v[2], v[3]};
-            q[1] = f32x4{v[4], v[5], v[6], v[7]};
+            const f32x4 a = {v[0], v[1], v[2], v[3]}, b = {v[4], v[5], v[6], v[7]};
+            if constexpr (STREAM) {
+                __builtin_nontemporal_store(a, q);
+                __builtin_nontemporal_store(b, q + 1);
+            } else {
+                q[0] = a;
+                q[1] = b;
+            }
         } else {
             u32x4 u;
 #pragma unroll
             for (int e = 0; e < 4; ++e)
                 u[e] = dt == MOE_DT_BF16 ? pack_bf16(v[2 * e], v[2 * e + 1])
                                          : pack_f16(v[2 * e], v[2 * e + 1]);
-            *reinterpret_cast<u32x4*>(static_cast<uint16_t*>(p) + i) = u;
+            u32x4* q = reinterpret_cast<u32x4*>(static_cast<uint16_t*>(p) + i);
+            if constexpr (STREAM) __builtin_nontemporal_store(u, q);
+            else *q = u;
         }
     } else {
 #pragma unroll

@@ -56,7 +56,7 @@ def close_codes(q, scale, n, mag, H, what):
 @pytest.mark.parametrize("dt", sorted(TYPES))
 @pytest.mark.parametrize("T,H", [(1, 1), (1, 6144), (3, 7), (5, 64), (2, 1003), (7, 8192),
                                  (2, 8200), (2, 16392), (2, 32768), (3, 8193), (2, 32767),
-                                 (260, 136)])
+                                 (260, 136), (300, 8192), (2200, 1000)])
 def test_norm(T, H, dt):
     say("block_norm", T, H, dt)
     rs = np.random.default_rng(H * 7 + T)
@@ -101,7 +101,7 @@ def test_residual(T, H, post, gate, r_t, y_t, w_t, n_t):
 
 @pytest.mark.parametrize("y_t,r_t", [("fp32", "bf16"), ("bf16", "bf16"), ("fp16", "fp32")])
 @pytest.mark.parametrize("T,k,H,E", [(1, 8, 6144, 256), (3, 1, 40, 4), (9, 3, 333, 5),
-                                     (2, 16, 128, 16), (65, 8, 264, 32)])
+                                     (2, 16, 128, 16), (65, 8, 264, 32), (520, 3, 4104, 8)])
 @pytest.mark.parametrize("shared", [0, 1, 2])
 def test_combine(T, k, H, E, shared, y_t, r_t):
     rs = np.random.default_rng(T + k + H)
@@ -157,7 +157,7 @@ def test_strides_and_offsets():
 
 def test_rows_do_not_depend_on_the_batch():
     """A row's bits are the same alone and among others, and run to run."""
-    T, H, k, E = 1030, 1024, 4, 16
+    T, H, k, E = 2100, 1024, 4, 16
     rs = np.random.default_rng(8)
     logits = torch.from_numpy(rs.standard_normal((T, E)).astype(np.float32)).to(DEV)
     _, tw, _, _, _, inv = moeq.route_permute(logits, k)
