@@ -5,9 +5,18 @@
 //   interleaved gate and up rows,  h[r, n] = silu(g) * u    (fp32)
 //
 // v_mfma_i32_16x16x64_i8 multiplies 16 weight rows (A: one 1024-byte tile, a
-// 16-byte load per lane) by up to 16 token rows (B: gathered 16-byte loads
-// from the caches).  The KS waves of a workgroup split the inputs and add
+// contiguous 16-byte load per lane) by up to 16 token rows (B: gathered 16-byte
+// loads from the caches).  The KS waves of a workgroup split the inputs and add
 // their int32 sums in LDS (integer sums: any order gives the same bits).
+//
+// The weights' stream bounds it.  Measured (us, weights from HBM): routed
+// experts, H 6144, I 2048, 8 of 256, gate/up + codes of h + down: 58 at one
+// token (302 MB), 337 at 8, 928 at 32 (6.2 GB: 6.6 TB/s, a read alone reaches
+// 6.1 to 7.0).  One 6144 x 6144 matrix at one token 9.8 (38 MB), 1024 x 1024 3.5.
+// Many experts stream best from one-wave workgroups (KS 1, 8 tiles in flight:
+// 889 us at 32 tokens against 951 with 2 x 2 waves, 967 with KS 4); a lone
+// matrix needs its inputs split to fill the chip (KS 4 with 2 row groups, 8 with
+// one below 256 row groups: 6144 -> 2048 5.9 us against 8.2 with KS 4).
 #include <type_traits>
 
 #include "i8_dev.h"

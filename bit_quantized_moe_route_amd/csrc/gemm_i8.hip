@@ -9,7 +9,21 @@
 //     read by one wave), the next 128 inputs in flight while the current are
 //     multiplied;
 //   * the BM x 128 token codes are gathered through registers into LDS,
-//     double-buffered, 16-byte chunks XOR-swizzled by row.
+//     double-buffered, 16-byte chunks XOR-swizzled by row.  (Direct-to-LDS loads
+//     make the compiler wait for all of them before any LDS read: 229 us against
+//     184 for the case below.)
+//
+// What bounds it: the matrix cores for one large matrix (4096 tokens, 6144 x
+// 6144: 144 to 150 us, 2.06 to 2.15 POP/s; the library's 8192^3 product reached
+// 2.03 on the same card); the weights' stream for routed experts, whose bytes
+// are read once a tile (8 of 256, H 6144, I 2048: 1.74 ms at 1024 tokens, 1.82
+// at 2048, 2.26 at 4096: 1.44 gate/up, 0.055 codes of h, 0.74 down.  The gate/up
+// pass there fetches 8.0 GB for 6.4 GB of weights, since half of the experts
+// have over 128 rows and their second tile finds two thirds of its weights in
+// L2; without its 268 MB of h stores it would take 1.22 ms, without its products
+// no less.  Tiles of 64 or 96 rows, two tiles in one workgroup, blocked weight
+// layouts and two stages in flight were all slower or no faster); the latency
+// of one workgroup per CU in between (500 tokens: 40 us for 6144 x 6144).
 #include <type_traits>
 
 #include "i8_dev.h"

@@ -18,7 +18,16 @@
  *                       y_shared                   -> out [T, H]
  *
  * (moe_layer_forward_shared runs the routed layer and its shared expert in
- * one call).
+ * one call).  Around the layer, and in 8-bit integers (weights with a scale per
+ * output channel, activations with one per token):
+ *
+ *   moe_block_norm      the norms before and after a block, with its gate, the
+ *                       residual stream, a routed layer's gated sum and the
+ *                       8-bit code of the result, in one pass
+ *   moe_quantize_i8     rows -> codes and scales
+ *   moe_linear_i8       a matrix product
+ *   moe_expert_ffn_i8   the routed experts' FFN, rows as moe_expert_ffn_q's
+ *   moe_shared_ffn_i8   one expert on every token
  *
  * Passages these calls follow (titles and sections of the source pages):
  *   - 256 routed experts per MoE layer, 8 active per token:
@@ -71,14 +80,16 @@
  *     unspecified results but no out-of-bounds access beyond the buffers'
  *     stated sizes for ids in range.  (With a token naming one expert twice,
  *     that expert can hold more than T rows; the decode-size FFN kernels,
- *     T < 128, compute the first T of them only.)
- *   - Operand range: the expert FFNs multiply on the matrix cores' fp16
+ *     T < 128, compute the first T of them only; moe_expert_ffn_i8 computes
+ *     every row.)
+ *   - Operand range: the expert FFNs of a moe_qlayer multiply on the matrix cores' fp16
  *     operands, so each activation x and each SwiGLU output h must lie in
  *     fp16's finite range, |v| <= 65504 (every bf16 value up to 65280 is
  *     exact there; below 2^-14 a value is rounded to fp16's subnormal grid,
  *     error < 2^-25).  A token with a value beyond the range gets a
  *     non-finite output row; the other tokens' rows are unaffected, since no
- *     product mixes two tokens.
+ *     product mixes two tokens.  The 8-bit calls take any finite fp32 value; a
+ *     result stored as fp16 overflows to an infinity beyond 65504.
  */
 #ifndef MOEQ_H
 #define MOEQ_H
