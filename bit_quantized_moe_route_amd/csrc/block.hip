@@ -236,7 +236,9 @@ void launch(const BlockRow& A, int64_t T, hipStream_t s) {
     // Results of 2M elements and more go past the caches (4096 rows of 6144 bf16
     // that were not in them: 26.2 -> 23.0 us for the norm alone, 116 -> 103 with
     // the gated sum of 8 rows each, which are then read past them too; fp32
-    // rows are not: 194 us against 181).
+    // rows are not: 194 us against 181).  A call that reads the results at once
+    // finds less of them: residual + code + residual 98.8 us against 96.5 with
+    // plain stores, gated sum + code 274.8 either way (284.5 with plain loads).
     const bool stream = V == 8 && T * A.H >= (int64_t)1 << 21;
     auto go = [&](auto comb) {
         constexpr int K = decltype(comb)::value;

@@ -607,9 +607,11 @@ typedef struct moe_i8_linear {
  *   x          [device] codes (x_dtype MOE_DT_I8, rows as moe_quantize_i8
  *              writes them, with x_scale [T]), or [T, K] of a float type,
  *              which the call codes as moe_quantize_i8 does (x_scale NULL).
- *   out        [device] [T, N] of out_dtype, rows ldo apart.
+ *   out        [device] [T, N] of out_dtype, rows ldo apart; overlaps no
+ *              operand.
  *   workspace  [device] >= moe_linear_i8_workspace_bytes(), 256-byte aligned;
  *              unused (NULL allowed) when x is codes.
+ *   A row's bits depend on nothing but the row and the matrix.
  */
 size_t moe_linear_i8_workspace_bytes(const moe_i8_linear* linear, int64_t T);
 int moe_linear_i8(const moe_i8_linear* linear, const void* x, int32_t x_dtype, int64_t ldx,
@@ -635,7 +637,7 @@ typedef struct moe_i8_layer {
  *               moe_quantize_i8) with down of e, scaled, rounded to y_dtype
  *   x, x_dtype, ldx, x_scale as for moe_linear_i8 (K = H); perm_src, offsets
  *   as for moe_expert_ffn_q; y_perm [device] [T*k, H] of y_dtype (fp32 for
- *   moe_combine; moe_block_norm takes every type).
+ *   moe_combine; moe_block_norm takes every type); it overlaps no operand.
  *   Any H and I from 1 to 131071.  workspace [device] >=
  *   moe_expert_ffn_i8_workspace_bytes(), 256-byte aligned.
  *
