@@ -125,7 +125,8 @@ __global__ __launch_bounds__(1024) void k_block(BlockRow A) {
 
     // ------------------------------------------------ the norm after
     // The sum of squares: by chunk, then 64 neighbouring chunks over lanes, then
-    // these in order, whatever part of the row a wave holds.
+    // these parts in order, or over lanes again where there are many: chains of at
+    // most 30 sums, and one order whatever part of the row a wave holds.
     auto norm = [&](float* part) {
         const int n64 = (H + 64 * V - 1) / (64 * V);
         float total = 0.f;
@@ -143,7 +144,12 @@ __global__ __launch_bounds__(1024) void k_block(BlockRow A) {
         if (n64 > 1) {
             __syncthreads();
             total = 0.f;
-            for (int i = 0; i < n64; ++i) total += part[i];
+            if (n64 <= 16) {
+                for (int i = 0; i < n64; ++i) total += part[i];
+            } else {
+                for (int i = threadIdx.x & 63; i < n64; i += 64) total += part[i];
+                total = wave_sum(total);
+            }
         }
         return 1.f / sqrtf(total / (float)H + b.eps);
     };

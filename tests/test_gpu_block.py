@@ -2,7 +2,8 @@
 
 Tolerance, from the kernel's arithmetic: everything is fp32 until one rounding
 to the output's type.  A sum of H squares adds at most 40 values in one chain
-(32 of a thread, 6 lane stages, the rest over waves), each rounding 2^-24, and
+(8 of a thread, 6 lane stages, then 16 parts in order or, where there are more,
+8 a lane and 6 lane stages), each rounding 2^-24, and
 enters as a square root (half); the other steps of an element are under 30
 roundings (k <= 16 products and sums among them).  64 * 2^-24 = 2^-18 of the
 sum of the terms' magnitudes covers them; half a step of the output type comes
