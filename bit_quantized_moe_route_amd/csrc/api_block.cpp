@@ -45,11 +45,12 @@ int check_codes(const std::string& fn, const char* name, const void* q, int64_t 
     return MOE_OK;
 }
 
-// The products' workgroups: at most rows / 128 + E tiles of rows (smaller tiles
-// are for fewer rows) by N / 256 of channels, in one launch of less than 2^31.
+// The products' tiles are 128 rows by 256 channels wherever they are many, and
+// no smaller than 32 rows for up to 64 rows of each expert: the workgroups of a
+// pass, 256 threads each, are one launch of less than 2^32 threads.
 int check_tiles(const std::string& fn, int64_t rows, int64_t E, int64_t N) {
-    const int64_t bm = rows > (int64_t)1 << 20 ? 128 : 32;
-    if ((rows / bm + E + 1) * (N / 64 + 1) >= kMaxRows - 4096)
+    const int64_t bm = rows > 64 * (int64_t)MOE_MAX_E ? 128 : 32;
+    if ((rows / bm + E + 1) * (N / 256 + 1) >= rows_of_launch(4) - 64)
         return fail(MOE_EUNSUPPORTED, fn + ": too many rows and channels for one call");
     return MOE_OK;
 }
@@ -281,6 +282,8 @@ int moe_pack_i8(const int8_t* codes, int64_t ld, int32_t N, int32_t K, void* pac
     set_error("");
     const std::string fn = "moe_pack_i8";
     if (moe_i8_matrix_bytes(N, K) == 0) return bad(fn, "bad N or K");
+    if (moe_i8_matrix_bytes(N, K) / kI8TileBytes >= 4 * (uint64_t)rows_of_launch(4))
+        return fail(MOE_EUNSUPPORTED, fn + ": the matrix is too large for one launch");
     if (ld < K) return bad(fn, "the row stride is below K");
     if (!codes || !packed) return bad(fn, "null pointer");
     if (!aligned(packed, 16)) return bad(fn, "packed must be 16-byte aligned");

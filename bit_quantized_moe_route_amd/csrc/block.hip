@@ -27,6 +27,7 @@ namespace {
 
 struct BlockRow {
     moe_block b;
+    int64_t t0;     // the launch's first row
     int H, nw;      // nw: waves of a row
 };
 
@@ -41,7 +42,7 @@ __global__ __launch_bounds__(1024) void k_block(BlockRow A) {
     __shared__ float red[2][V == 8 ? 64 : 512];
     __shared__ uint32_t red_max[16];
     const moe_block& b = A.b;
-    const int64_t t = blockIdx.x;
+    const int64_t t = A.t0 + blockIdx.x;
     const int H = A.H, nt = A.nw * 64;
     const bool has_y = COMB || b.y;
     float v[NCH][V];
@@ -237,7 +238,7 @@ __global__ __launch_bounds__(1024) void k_block(BlockRow A) {
 }
 
 template <int V, int NCH>
-void launch(const BlockRow& A, int64_t T, hipStream_t s) {
+void launch(BlockRow& A, int64_t T, hipStream_t s) {
     constexpr int C = V == 1 && NCH > 8 ? 1 : 4;
     // Results of 2M elements and more go past the caches (4096 rows of 6144 bf16
     // that were not in them: 26.2 -> 23.0 us for the norm alone, 116 -> 103 with
@@ -249,9 +250,13 @@ void launch(const BlockRow& A, int64_t T, hipStream_t s) {
     auto go = [&](auto comb) {
         constexpr int K = decltype(comb)::value;
         constexpr int S1 = V == 8 ? 1 : 0, S2 = V == 8 && K ? 2 : S1;
-        if (!stream) k_block<V, NCH, K, 0><<<(unsigned)T, A.nw * 64, 0, s>>>(A);
-        else if (A.b.y_dtype == MOE_DT_F32) k_block<V, NCH, K, S1><<<(unsigned)T, A.nw * 64, 0, s>>>(A);
-        else k_block<V, NCH, K, S2><<<(unsigned)T, A.nw * 64, 0, s>>>(A);
+        const int64_t most = rows_of_launch(A.nw);
+        for (A.t0 = 0; A.t0 < T; A.t0 += most) {
+            const unsigned n = (unsigned)(T - A.t0 < most ? T - A.t0 : most);
+            if (!stream) k_block<V, NCH, K, 0><<<n, A.nw * 64, 0, s>>>(A);
+            else if (A.b.y_dtype == MOE_DT_F32) k_block<V, NCH, K, S1><<<n, A.nw * 64, 0, s>>>(A);
+            else k_block<V, NCH, K, S2><<<n, A.nw * 64, 0, s>>>(A);
+        }
     };
     if (A.b.k > 0) go(std::integral_constant<int, C>{});
     else go(std::integral_constant<int, 0>{});
@@ -264,7 +269,7 @@ int launch_block(const moe_block& b, int64_t T, int32_t H, bool vec8, void* stre
     hipStream_t s = reinterpret_cast<hipStream_t>(stream);
     const int V = vec8 ? 8 : 1;
     const int nch = (H + V - 1) / V;
-    BlockRow A{b, H, 1};
+    BlockRow A{b, 0, H, 1};
     auto waves = [&](int per) { return (nch + 64 * per - 1) / (64 * per); };
     // As many threads as a row has chunks, up to 1024 (one token, H 6144: 3.2 us
     // against 4.0 with two chunks a thread; 4096 tokens from HBM, norm after and

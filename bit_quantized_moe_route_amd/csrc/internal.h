@@ -211,6 +211,8 @@ int launch_layer_small_shared(const LayerView& L, int fmt, const LayerView& SL,
                               float* sh_part, float* out, void* stream);
 int launch_dequant(const LayerView& L, int fmt, int32_t rec_index, int32_t proj,
                    float* out, void* stream);
+// A launch holds less than 2^32 threads: the most workgroups of nw waves in one.
+inline int64_t rows_of_launch(int nw) { return (((int64_t)1 << 32) - 1) / (64 * nw); }
 // Block norms (vec8: H % 8 == 0 and every row of every operand 16-byte aligned).
 int launch_block(const moe_block& b, int64_t T, int32_t H, bool vec8, void* stream);
 // Rows to 8-bit codes with a scale each; codes padded with zeros to a multiple

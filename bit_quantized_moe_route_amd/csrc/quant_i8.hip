@@ -17,7 +17,7 @@ namespace {
 
 struct QuantArgs {
     const void* x;
-    int64_t ldx, ldq, T;
+    int64_t ldx, ldq, T, t0;   // t0: the launch's first row
     int8_t* q;
     float* scale;
     int dt, K, nw;   // nw: waves of a row
@@ -38,7 +38,7 @@ template <int V, int NCH>
 __global__ __launch_bounds__(1024) void k_quantize(QuantArgs A) {
     __shared__ uint32_t red[16];
     const int tid = threadIdx.x, nt = A.nw * 64;
-    const int64_t t = blockIdx.x;
+    const int64_t t = A.t0 + blockIdx.x;
     int8_t* q = A.q + t * A.ldq;
     uint32_t amax = 0u;
     if constexpr (NCH > 0) {
@@ -115,7 +115,11 @@ void launch_q(QuantArgs A, hipStream_t s) {
     auto go = [&](auto tag, int per) {
         constexpr int NCH = decltype(tag)::value;
         A.nw = per ? waves(per) : 16;
-        k_quantize<V, NCH><<<(unsigned)A.T, A.nw * 64, 0, s>>>(A);
+        const int64_t most = rows_of_launch(A.nw);
+        for (A.t0 = 0; A.t0 < A.T; A.t0 += most) {
+            const int64_t n = A.T - A.t0 < most ? A.T - A.t0 : most;
+            k_quantize<V, NCH><<<(unsigned)n, A.nw * 64, 0, s>>>(A);
+        }
     };
     constexpr int C0 = V == 8 ? 1 : 2, C1 = V == 8 ? 4 : 16;
     if (waves(C0) <= 16) go(std::integral_constant<int, C0>{}, C0);
@@ -128,7 +132,7 @@ void launch_q(QuantArgs A, hipStream_t s) {
 int launch_quantize_i8(const void* x, int dt, int64_t ldx, int64_t T, int32_t K, int8_t* q,
                        int64_t ldq, float* scale, bool vec8, void* stream) {
     hipStream_t s = reinterpret_cast<hipStream_t>(stream);
-    QuantArgs A{x, ldx, ldq, T, q, scale, dt, K, 1};
+    QuantArgs A{x, ldx, ldq, T, 0, q, scale, dt, K, 1};
     if (vec8) launch_q<8>(A, s);
     else launch_q<1>(A, s);
     MOEQ_CHECK_LAUNCH();

@@ -183,6 +183,16 @@ def test_matrix_sizes_and_pack_refusals():
     refused("moe_pack_i8_expert", P, P, P, 16, 16, P + 8, P, None)
 
 
+def test_calls_past_one_launch_are_refused():
+    """Products of 2^32 threads and more, and a matrix of 64 GiB."""
+    refused("moe_pack_i8", P, 1 << 12, 1 << 24, 1 << 12, P, None, status=moeq.MOE_EUNSUPPORTED)
+    refused("moe_linear_i8", lin(N=1 << 16), P, 4, 64, P, 1 << 24, P, 2, 1 << 16, None, 0, None,
+            status=moeq.MOE_EUNSUPPORTED, says="too many")
+    refused("moe_expert_ffn_i8", lay(H=1 << 16, I=64, w13_stride=1 << 24, w2_stride=1 << 24), P, 2,
+            1 << 16, None, P, P, 1 << 23, 4, P, 2, P, 1 << 20, None, status=moeq.MOE_EUNSUPPORTED,
+            says="too many")
+
+
 def lin(**kw):
     d = dict(N=32, K=64, w=P, w_scale=P)
     d.update(kw)

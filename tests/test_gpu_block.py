@@ -176,6 +176,27 @@ def test_rows_do_not_depend_on_the_batch():
             assert torch.equal(a[0], b[t])
 
 
+def test_more_rows_than_one_launch_holds():
+    """A launch ends at 2^32 threads, 2^26 rows of one wave each: the rows behind
+    it, and those beside the border, are done all the same."""
+    T, n = (1 << 26) + 37, 1 << 26
+    x = torch.ones((T, 1), dtype=torch.bfloat16, device=DEV)
+    x[-50:, 0] = torch.arange(1, 51, device=DEV)
+    w = torch.full((1,), 2.0, dtype=torch.bfloat16, device=DEV)
+    # rows of one element: n = w * r / sqrt(r^2), r' = r + 3
+    r2, out = moeq.block_residual(x, torch.full_like(x, 3.0), w, eps=0.0)
+    assert torch.all(out == 2.0)
+    assert torch.equal(r2[-50:, 0], torch.arange(4, 54, device=DEV).to(torch.bfloat16))
+    assert torch.all(r2[:-50] == 4.0)
+    del r2, out
+    # codes 127 of rows of one element
+    q, s = moeq.quantize_i8(x)
+    assert torch.all(q[:, 0] == 127) and torch.all(q[n - 64:, 1:] == 0)
+    a = x[-50:, 0].to(torch.float64)
+    assert torch.all((s[-50:].to(torch.float64) * 127 - a).abs() <= 2.0 ** -24 * a)
+    assert torch.all(s[:-50] == s[0])
+
+
 def test_non_finite_rows_stay_apart():
     T, H = 6, 72
     rs = np.random.default_rng(9)
