@@ -124,14 +124,17 @@ _fns = {}
 
 def _bind(L):
     """The library's functions and torch's stream lookup (the raw one where
-    this torch has it: a Stream object costs as much as a launch)."""
+    this torch has it: a Stream object costs as much as a launch).  The table is
+    replaced whole: another thread's call keeps the one it looked up."""
+    global _fns
     torch = _torch()
-    _fns.clear()
-    _fns.update({n: getattr(L, n) for n in PROTOS})
-    _fns["lib"] = L
-    _fns["stream"] = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+    f = {n: getattr(L, n) for n in PROTOS}
+    f["lib"] = L
+    f["stream"] = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
         lambda i: torch.cuda.current_stream(i).cuda_stream)
-    _fns["device"] = torch.cuda.current_device
+    f["device"] = torch.cuda.current_device
+    _fns = f
+    return f
 
 
 def _call(name, dev, *args):
@@ -139,7 +142,7 @@ def _call(name, dev, *args):
     L = lib()
     f = _fns
     if f.get("lib") is not L:
-        _bind(L)
+        f = _bind(L)
     i = dev.index
     if i == f["device"]():
         st = f[name](*args, f["stream"](i))

@@ -307,3 +307,12 @@ def test_row_checks():
     with pytest.raises(ValueError, match="fp32, bf16 or fp16"):
         mb._dt(torch.float64)
     assert [mb.codes_width(k) for k in (1, 64, 65, 6144)] == [64, 64, 128, 6144]
+
+
+def test_function_table_is_replaced_whole():
+    """A thread that looked the table up keeps a whole one while another binds."""
+    first = mb._bind(moeq.lib())
+    names = set(first)
+    second = mb._bind(moeq.lib())
+    assert second is not first and set(first) == names == set(second)
+    assert mb._fns is second and first["lib"] is moeq.lib()
