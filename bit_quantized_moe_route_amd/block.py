@@ -230,6 +230,8 @@ def _block(dev, T, H, r, y, w, k, inv_perm, topk_w, y_shared, shared_gate, post_
     if codes:
         q, q_ld, scale = _codes_like(T, H, q, scale, dev)
         q_p, qs_p = q.data_ptr(), scale.data_ptr()
+    elif q is not None or scale is not None:
+        raise ValueError("q and scale go with codes=True")
     if T:
         _call("moe_block_norm", dev,
               _BLOCK.pack(y_p, y_ld, inv_p, tw_p, ys_p, ys_ld, sg_p, pw_p, g_p, g_ld, g_lh, r_p,

@@ -316,3 +316,11 @@ def test_function_table_is_replaced_whole():
     second = mb._bind(moeq.lib())
     assert second is not first and set(first) == names == set(second)
     assert mb._fns is second and first["lib"] is moeq.lib()
+
+
+def test_code_outputs_need_codes():
+    r, w = torch.zeros((2, 64)), torch.ones(64)
+    for kw in (dict(q=torch.zeros((2, 64), dtype=torch.int8)), dict(scale=torch.zeros(2))):
+        with pytest.raises(ValueError, match="codes=True"):
+            mb._block(r.device, 2, 64, r, None, w, 0, None, None, None, None, None, None, 1.0, 1.0,
+                      1e-5, 0.0, None, None, None, False, kw.get("q"), kw.get("scale"))
