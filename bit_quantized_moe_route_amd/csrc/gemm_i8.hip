@@ -314,7 +314,8 @@ __global__ __launch_bounds__(64 * CW * KP, 2) void k_gemm_i8(I8Pass A, int ngrou
                 typedef T T2 __attribute__((ext_vector_type(2)));
                 T* o = static_cast<T*>(A.out) + ch;
                 rows([&](float q, int a0, int a1, int64_t at) {
-                    const T y0 = (T)(q * s0 * (float)a0 + b0), y1 = (T)(q * s1 * (float)a1 + b1);
+                    const T y0 = as_type<T>(q * s0 * (float)a0 + b0);
+                    const T y1 = as_type<T>(q * s1 * (float)a1 + b1);
                     if (pairs) {
                         *reinterpret_cast<T2*>(o + at) = T2{y0, y1};
                     } else {

@@ -1,6 +1,8 @@
 // Device helpers of the 8-bit integer products.
 #pragma once
 
+#include <type_traits>
+
 #include "elem_dev.h"
 
 namespace moeq {
@@ -29,6 +31,15 @@ __device__ __forceinline__ int uniform(int v) { return __builtin_amdgcn_readfirs
 // within an ulp or two of fp32), far inside what the 8-bit code of h resolves.
 __device__ __forceinline__ float silu_mul(float g, float u) {
     return g * __builtin_amdgcn_rcpf(1.f + __expf(-g)) * u;
+}
+
+// y as T.  An fp16 is rounded from the fp32 value like everywhere else: folded
+// into one instruction with the sum that makes y, it would be rounded once where
+// the other kernels round twice, and a row's bits would follow the kernel.
+template <typename T>
+__device__ __forceinline__ T as_type(float y) {
+    if constexpr (std::is_same_v<T, _Float16>) asm("" : "+v"(y));
+    return (T)y;
 }
 
 // Offsets of experts e0 + 64 c + lane, c < 4, all loads in flight together.

@@ -480,3 +480,55 @@ def test_routed_oracle_of_the_whole_layer():
     err = np.abs(r["out"].cpu().numpy() - out)
     rel = np.sqrt((err ** 2).mean(1) / (out * out).mean(1))
     assert rel.max() <= 0.046, rel.max()
+
+
+@pytest.mark.parametrize("dt", sorted(TYPES))
+def test_rows_do_not_depend_on_the_batch(dt):
+    """A row's bits are the same in every kernel that its batch leads to."""
+    rs = np.random.default_rng(31)
+    K, N, T = 712, 1330, 700
+    lin = moeq.I8Linear(codes(rs, (N, K)), scales(rs, N), rnd(rs, (N,), torch.float32))
+    shared = moeq.I8Layer(codes(rs, (1, 2 * N, K)), scales(rs, 2 * N).view(1, -1),
+                          codes(rs, (1, K, N)), scales(rs, K).view(1, -1))
+    x = rnd(rs, (T, K), TYPES[dt], 2.0)
+    full, ffn = moeq.linear_i8(lin, x), moeq.shared_ffn_i8(shared, x)
+    for a, n in ((0, 1), (5, 4), (300, 16), (1, 30), (400, 120), (350, 350)):
+        say("rows", dt, a, n)
+        assert torch.equal(moeq.linear_i8(lin, x[a:a + n]), full[a:a + n])
+        assert torch.equal(moeq.shared_ffn_i8(shared, x[a:a + n]), ffn[a:a + n])
+
+
+def test_graphs_of_the_products():
+    """Two graphs, each with its own memory, replayed in turn with eager calls
+    between them, on new inputs."""
+    rs = np.random.default_rng(32)
+    E, H, I, k = 8, 328, 200, 2
+    layer = moeq.I8Layer(codes(rs, (E, 2 * I, H)), scales(rs, E * 2 * I).view(E, -1),
+                         codes(rs, (E, H, I)), scales(rs, E * H).view(E, -1))
+    lin = moeq.I8Linear(codes(rs, (264, H)), scales(rs, 264))
+    sets = []
+    for T in (3, 150):
+        x = rnd(rs, (T, H), torch.bfloat16)
+        logits = rnd(rs, (T, E), torch.float32)
+        _, tw, _, off, src, inv = moeq.route_permute(logits, k)
+
+        def step(x=x, tw=tw, off=off, src=src, inv=inv):
+            y = moeq.expert_ffn_i8(layer, x, src, off, k)
+            r, n = moeq.combine_residual(x, y, inv, tw, torch.ones_like(x[0]))
+            return moeq.linear_i8(lin, n), r
+
+        for _ in range(2):
+            step()
+        torch.cuda.synchronize()
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            out = step()
+        sets.append((T, x, step, g, out))
+    for i in range(4):
+        for T, x, step, g, out in sets:
+            say("replay", i, T)
+            x.copy_(rnd(rs, (T, H), torch.bfloat16))
+            g.replay()
+            torch.cuda.synchronize()
+            for a, b in zip(out, step()):
+                assert torch.equal(a, b), (i, T)
