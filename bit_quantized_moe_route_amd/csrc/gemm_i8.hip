@@ -22,8 +22,10 @@
 // have over 128 rows and their second tile finds two thirds of its weights in
 // L2; without its 268 MB of h stores it would take 1.22 ms, without its products
 // no less.  Tiles of 64 or 96 rows, two tiles in one workgroup, blocked weight
-// layouts and two stages in flight were all slower or no faster); the latency
-// of one workgroup per CU in between (500 tokens: 40 us for 6144 x 6144).
+// layouts and two stages in flight were all slower or no faster); the weights'
+// loads of one workgroup per CU in between (500 tokens, 6144 x 6144: 40 us, 26
+// without them; 8 waves a workgroup, 3 or 4 stages in flight, another first input
+// for each workgroup: no faster).
 #include <type_traits>
 
 #include "i8_dev.h"
