@@ -270,7 +270,15 @@ int launch_i8(const I8Pass& p, bool pair, void* stream) {
         else if (pair) pick<true, 4>(p, ngroups, slots, mean, s);
         else pick<false, 4>(p, ngroups, slots, mean, s);
     } else {
-        if (mean > (slots > 1 ? 12 : 16)) return launch_gemm_i8(p, pair, stream);
+        // More rows go to the GEMM: from 17 of one matrix, unless this kernel's
+        // workgroups, one for every 16 rows, find a CU each (us here / there:
+        // 6144 -> 4096 at 32 rows 12.2 / 15.5, at 33 18.0 / 14.2; 6144 -> 256 at 200
+        // rows 7.3 / 9.7; 6144 x 6144 at 32 21.2 / 17.1); from 13 of an expert on
+        // average, since experts differ.
+        const int ng = pair || slots * ngroups >= 256 ? 2 : 1;     // as pick() has it
+        const int64_t wgs = (ngroups + ng - 1) / ng * ((mean + 15) / 16);
+        if (slots > 1 ? mean > 12 : mean > 16 && wgs > 256)
+            return launch_gemm_i8(p, pair, stream);
         if (pair) pick<true, 0>(p, ngroups, slots, mean, s);
         else pick<false, 0>(p, ngroups, slots, mean, s);
     }
