@@ -35,11 +35,15 @@ struct BlockRow {
 // STREAM: more rows than the caches hold; results (1) and the rows of a gated
 // sum (2) go past them.  Everything the row needs is loaded before the first reduction (EARLY), while
 // it fits the registers of a workgroup of 1024 threads.
-template <int V, int NCH, int COMB, int STREAM>
+// ANY: rows that start off 16 bytes or end inside a chunk.  The last chunk then
+// ends at the row's end and shares `lo` elements with the one before, which owns
+// them: the other neither adds nor stores them (and may find them overwritten,
+// where results go over operands).
+template <int V, int NCH, int COMB, int STREAM, bool ANY>
 __global__ __launch_bounds__(1024) void k_block(BlockRow A) {
     constexpr bool EARLY = V * NCH <= 8;
     constexpr int NE = EARLY ? NCH : 1;
-    __shared__ float red[2][V == 8 ? 64 : 512];
+    __shared__ float red[2][64];
     __shared__ uint32_t red_max[16];
     const moe_block& b = A.b;
     const int64_t t = A.t0 + blockIdx.x;
@@ -47,15 +51,24 @@ __global__ __launch_bounds__(1024) void k_block(BlockRow A) {
     const bool has_y = COMB || b.y;
     float v[NCH][V];
     Raw<V> rr[NE], rp[NE], rg[NE], rn[NE];
-    // threads past the row read its start and hold zeros
+    // a thread's elements at(c) + lo(c) .. at(c) + V: none past the row, where it
+    // reads the last ones
     auto place = [&](int c) { return (c * nt + (int)threadIdx.x) * V; };
-    auto at = [&](int c) { return place(c) < H ? place(c) : 0; };
-    auto load_r = [&](int c, Raw<V>& x) { if (b.r) x.load(b.r, b.r_dtype, t * b.ld_r + at(c)); };
-    auto load_p = [&](int c, Raw<V>& x) { if (b.post_w) x.load(b.post_w, b.w_dtype, at(c)); };
-    auto load_g = [&](int c, Raw<V>& x) {
-        if (b.gate && b.gate_ld_h) x.load(b.gate, b.gate_dtype, t * b.gate_ld_t + at(c));
+    auto at = [&](int c) { return min(place(c), H - V); };
+    auto lo = [&](int c) { return place(c) - at(c); };
+    auto load_r = [&](int c, Raw<V>& x) {
+        if (b.r) x.template load<false, ANY>(b.r, b.r_dtype, t * b.ld_r + at(c));
     };
-    auto load_n = [&](int c, Raw<V>& x) { if (b.pre_w) x.load(b.pre_w, b.w_dtype, at(c)); };
+    auto load_p = [&](int c, Raw<V>& x) {
+        if (b.post_w) x.template load<false, ANY>(b.post_w, b.w_dtype, at(c));
+    };
+    auto load_g = [&](int c, Raw<V>& x) {
+        if (b.gate && b.gate_ld_h)
+            x.template load<false, ANY>(b.gate, b.gate_dtype, t * b.gate_ld_t + at(c));
+    };
+    auto load_n = [&](int c, Raw<V>& x) {
+        if (b.pre_w) x.template load<false, ANY>(b.pre_w, b.w_dtype, at(c));
+    };
     const float gate1 = b.gate && !b.gate_ld_h ? load_elem(b.gate, b.gate_dtype, t * b.gate_ld_t)
                                                : 1.f;
 
@@ -64,12 +77,13 @@ __global__ __launch_bounds__(1024) void k_block(BlockRow A) {
     if constexpr (COMB == 0) {
         if (b.y) {
 #pragma unroll
-            for (int c = 0; c < NCH; ++c) ry[c].load(b.y, b.y_dtype, t * b.ld_y + at(c));
+            for (int c = 0; c < NCH; ++c) ry[c].template load<false, ANY>(b.y, b.y_dtype, t * b.ld_y + at(c));
         }
     } else if (b.y_shared) {
 #pragma unroll
         for (int c = 0; c < NCH; ++c)
-            ry[c].load(b.y_shared, b.y_shared_dtype, t * b.ld_y_shared + at(c));
+            ry[c].template load<false, ANY>(b.y_shared, b.y_shared_dtype,
+                                            t * b.ld_y_shared + at(c));
     }
     if constexpr (EARLY) {
 #pragma unroll
@@ -98,7 +112,8 @@ __global__ __launch_bounds__(1024) void k_block(BlockRow A) {
             for (int c = 0; c < NCH; ++c) {
                 Raw<V> y[COMB];
 #pragma unroll
-                for (int u = 0; u < COMB; ++u) y[u].template load<STREAM == 2>(b.y, b.y_dtype, row[u] + at(c));
+                for (int u = 0; u < COMB; ++u)
+                    y[u].template load<STREAM == 2, ANY>(b.y, b.y_dtype, row[u] + at(c));
 #pragma unroll
                 for (int u = 0; u < COMB; ++u) {
                     if (j0 + u >= b.k) break;
@@ -134,9 +149,13 @@ __global__ __launch_bounds__(1024) void k_block(BlockRow A) {
 #pragma unroll
         for (int c = 0; c < NCH; ++c) {
             float ss = 0.f;
-            if (place(c) < H)
+            if (lo(c) < V) {
 #pragma unroll
-                for (int e = 0; e < V; ++e) ss += v[c][e] * v[c][e];
+                for (int e = 0; e < V; ++e) {
+                    const float x = ANY && e < lo(c) ? 0.f : v[c][e];
+                    ss += x * x;
+                }
+            }
             ss = wave_sum(ss);
             if (c == 0) total = ss;          // the whole row where it is one such part
             const int i = c * A.nw + ((int)threadIdx.x >> 6);
@@ -191,8 +210,9 @@ __global__ __launch_bounds__(1024) void k_block(BlockRow A) {
             for (int e = 0; e < V; ++e)
                 v[c][e] = has_y ? b.r_scale * f[e] + v[c][e] : b.r_scale * f[e];
         }
-        if (b.r_out && place(c) < H)
-            store_f32<V, (STREAM > 0)>(b.r_out, b.r_dtype, t * b.ld_r_out + place(c), v[c]);
+        if (b.r_out && lo(c) < V)
+            store_from<V, (STREAM > 0), ANY>(b.r_out, b.r_dtype, t * b.ld_r_out + at(c), v[c],
+                                             lo(c));
     }
     if (!b.n_out && !b.q_out) return;
 
@@ -209,10 +229,12 @@ __global__ __launch_bounds__(1024) void k_block(BlockRow A) {
 #pragma unroll
             for (int e = 0; e < V; ++e) v[c][e] = v[c][e] * rstd * (b.w_offset + f[e]);
         }
-        if (place(c) >= H) continue;
-        if (b.n_out) store_f32<V, (STREAM > 0)>(b.n_out, b.n_dtype, t * b.ld_n + place(c), v[c]);
+        if (lo(c) >= V) continue;
+        if (b.n_out)
+            store_from<V, (STREAM > 0), ANY>(b.n_out, b.n_dtype, t * b.ld_n + at(c), v[c], lo(c));
 #pragma unroll
-        for (int e = 0; e < V; ++e) amax = max(amax, __float_as_uint(v[c][e]) & 0x7fffffffu);
+        for (int e = 0; e < V; ++e)
+            if (!ANY || e >= lo(c)) amax = max(amax, __float_as_uint(v[c][e]) & 0x7fffffffu);
     }
     if (!b.q_out) return;
 
@@ -223,23 +245,23 @@ __global__ __launch_bounds__(1024) void k_block(BlockRow A) {
     int8_t* q = b.q_out + t * b.ld_q;
 #pragma unroll
     for (int c = 0; c < NCH; ++c) {
-        const int h = place(c);
-        if (h >= H) continue;
-        if constexpr (V == 8) {
-            const uint2 u = {pack_codes4(&v[c][0], rc.mul), pack_codes4(&v[c][4], rc.mul)};
-            *reinterpret_cast<uint2*>(q + h) = u;
+        if (lo(c) >= V) continue;
+        if (V == 8 && (!ANY || lo(c) == 0)) {
+            const uint2 u = {pack_codes4(&v[c][0], rc.mul), pack_codes4(&v[c][V / 2], rc.mul)};
+            *reinterpret_cast<uint2*>(q + at(c)) = u;
         } else {
 #pragma unroll
-            for (int e = 0; e < V; ++e) q[h + e] = (int8_t)code_of(v[c][e], rc.mul);
+            for (int e = 0; e < V; ++e)
+                if (e >= lo(c)) q[at(c) + e] = (int8_t)code_of(v[c][e], rc.mul);
         }
     }
     const int pad = (H + 63) / 64 * 64 - H;
     if ((int)threadIdx.x < pad) q[H + threadIdx.x] = 0;
 }
 
-template <int V, int NCH>
+template <int V, int NCH, bool ANY>
 void launch(BlockRow& A, int64_t T, hipStream_t s) {
-    constexpr int C = V == 1 && NCH > 8 ? 1 : 4;
+    constexpr int C = 4;
     // Results of 2M elements and more go past the caches (4096 rows of 6144 bf16
     // that were not in them: 26.2 -> 23.0 us for the norm alone, 116 -> 103 with
     // the gated sum of 8 rows each, which are then read past them too; fp32
@@ -253,9 +275,9 @@ void launch(BlockRow& A, int64_t T, hipStream_t s) {
         const int64_t most = rows_of_launch(A.nw);
         for (A.t0 = 0; A.t0 < T; A.t0 += most) {
             const unsigned n = (unsigned)(T - A.t0 < most ? T - A.t0 : most);
-            if (!stream) k_block<V, NCH, K, 0><<<n, A.nw * 64, 0, s>>>(A);
-            else if (A.b.y_dtype == MOE_DT_F32) k_block<V, NCH, K, S1><<<n, A.nw * 64, 0, s>>>(A);
-            else k_block<V, NCH, K, S2><<<n, A.nw * 64, 0, s>>>(A);
+            if (!stream) k_block<V, NCH, K, 0, ANY><<<n, A.nw * 64, 0, s>>>(A);
+            else if (A.b.y_dtype == MOE_DT_F32) k_block<V, NCH, K, S1, ANY><<<n, A.nw * 64, 0, s>>>(A);
+            else k_block<V, NCH, K, S2, ANY><<<n, A.nw * 64, 0, s>>>(A);
         }
     };
     if (A.b.k > 0) go(std::integral_constant<int, C>{});
@@ -267,24 +289,23 @@ void launch(BlockRow& A, int64_t T, hipStream_t s) {
 // vec8: every operand's rows start on 16 bytes and H is a multiple of 8.
 int launch_block(const moe_block& b, int64_t T, int32_t H, bool vec8, void* stream) {
     hipStream_t s = reinterpret_cast<hipStream_t>(stream);
-    const int V = vec8 ? 8 : 1;
-    const int nch = (H + V - 1) / V;
     BlockRow A{b, 0, H, 1};
-    auto waves = [&](int per) { return (nch + 64 * per - 1) / (64 * per); };
+    auto waves = [&](int per) { return (H + 512 * per - 1) / (512 * per); };
     // As many threads as a row has chunks, up to 1024 (one token, H 6144: 3.2 us
     // against 4.0 with two chunks a thread; 4096 tokens from HBM, norm after and
-    // before: 50 against 54).  Rows off 16 bytes: two elements a thread for few
-    // rows, four for many (333 / 4096 rows of 1003 fp32: 5.2 / 14.2 us with two,
-    // 6.1 / 11.8 with four).  The bits are the same.
-    if (vec8) {
-        if (waves(1) <= 16) { A.nw = waves(1); launch<8, 1>(A, T, s); }
-        else if (waves(2) <= 16) { A.nw = waves(2); launch<8, 2>(A, T, s); }
-        else { A.nw = waves(4); launch<8, 4>(A, T, s); }
-    } else {
-        if (waves(2) <= 16 && T < 1024) { A.nw = waves(2); launch<1, 2>(A, T, s); }
-        else if (waves(4) <= 16) { A.nw = waves(4); launch<1, 4>(A, T, s); }
-        else { A.nw = waves(32); launch<1, 32>(A, T, s); }
-    }
+    // before: 50 against 54).  Rows off 16 bytes go by the same chunks (norm after
+    // and before, one token / 4096 tokens of 6145 bf16: 5.6 / 77 us against 42 / 224
+    // element by element; 333 rows of 1003 fp32 5.0 against 6.0; 1008 takes 4.3).
+    // The bits are the same in all of them.
+    auto go = [&](auto any) {
+        constexpr bool ANY = decltype(any)::value;
+        if (waves(1) <= 16) { A.nw = waves(1); launch<8, 1, ANY>(A, T, s); }
+        else if (waves(2) <= 16) { A.nw = waves(2); launch<8, 2, ANY>(A, T, s); }
+        else { A.nw = waves(4); launch<8, 4, ANY>(A, T, s); }
+    };
+    if (vec8) go(std::false_type{});
+    else if (H >= 8) go(std::true_type{});
+    else launch<1, 1, false>(A, T, s);
     MOEQ_CHECK_LAUNCH();
     return MOE_OK;
 }

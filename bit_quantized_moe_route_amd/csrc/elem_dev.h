@@ -3,6 +3,8 @@
 // fp32, rounding stores, and reductions over a workgroup.  gfx950 only.
 #pragma once
 
+#include <type_traits>
+
 #include "dev_common.h"
 
 namespace moeq {
@@ -15,21 +17,35 @@ struct Raw8 {
     u32x4 a, b;
 };
 
-template <bool STREAM = false>
-__device__ __forceinline__ u32x4 load16(const u32x4* q) {
+// 16 bytes at an element's own alignment (ANY), which the memory path takes as
+// they are, or at 16; STREAM: past the caches.
+typedef uint32_t u32x4_any __attribute__((ext_vector_type(4), aligned(2)));
+
+template <bool STREAM = false, bool ANY = false>
+__device__ __forceinline__ u32x4 load16(const void* p) {
+    using Q = std::conditional_t<ANY, u32x4_any, u32x4>;
+    const Q* q = static_cast<const Q*>(p);
     if constexpr (STREAM) return __builtin_nontemporal_load(q);
     return *q;
 }
 
-template <bool STREAM = false>
+template <bool STREAM = false, bool ANY = false>
+__device__ __forceinline__ void store16(void* p, u32x4 u) {
+    using Q = std::conditional_t<ANY, u32x4_any, u32x4>;
+    Q* q = static_cast<Q*>(p);
+    if constexpr (STREAM) __builtin_nontemporal_store((Q)u, q);
+    else *q = u;
+}
+
+template <bool STREAM = false, bool ANY = false>
 __device__ __forceinline__ Raw8 load_raw8(const void* p, int dt, int64_t i) {
     Raw8 r;
     if (dt == MOE_DT_F32) {
-        const u32x4* q = reinterpret_cast<const u32x4*>(static_cast<const float*>(p) + i);
-        r.a = load16<STREAM>(q);
-        r.b = load16<STREAM>(q + 1);
+        const float* q = static_cast<const float*>(p) + i;
+        r.a = load16<STREAM, ANY>(q);
+        r.b = load16<STREAM, ANY>(q + 4);
     } else {
-        r.a = load16<STREAM>(reinterpret_cast<const u32x4*>(static_cast<const uint16_t*>(p) + i));
+        r.a = load16<STREAM, ANY>(static_cast<const uint16_t*>(p) + i);
         r.b = u32x4{0u, 0u, 0u, 0u};
     }
     return r;
@@ -62,22 +78,22 @@ __device__ __forceinline__ float load_elem(const void* p, int dt, int64_t i) {
     return (float)__builtin_bit_cast(_Float16, u);
 }
 
-// V elements (8: one aligned vector, 1: a scalar) as loaded, and as fp32.
+// V elements (8: one vector, 1: a scalar) as loaded, and as fp32.
 template <int V>
 struct Raw;
 template <>
 struct Raw<8> {
     Raw8 r;
-    template <bool STREAM = false>
+    template <bool STREAM = false, bool ANY = false>
     __device__ __forceinline__ void load(const void* p, int dt, int64_t i) {
-        r = load_raw8<STREAM>(p, dt, i);
+        r = load_raw8<STREAM, ANY>(p, dt, i);
     }
     __device__ __forceinline__ void f32(int dt, float (&v)[8]) const { raw_to_f32(r, dt, v); }
 };
 template <>
 struct Raw<1> {
     uint32_t r;
-    template <bool STREAM = false>
+    template <bool STREAM = false, bool ANY = false>
     __device__ __forceinline__ void load(const void* p, int dt, int64_t i) {
         r = dt == MOE_DT_F32 ? static_cast<const uint32_t*>(p)[i]
                              : static_cast<const uint16_t*>(p)[i];
@@ -89,10 +105,10 @@ struct Raw<1> {
     }
 };
 
-template <int V>
+template <int V, bool ANY = false>
 __device__ __forceinline__ void load_f32(const void* p, int dt, int64_t i, float (&v)[V]) {
     if constexpr (V == 8) {
-        raw_to_f32(load_raw8(p, dt, i), dt, v);
+        raw_to_f32(load_raw8<false, ANY>(p, dt, i), dt, v);
     } else {
 #pragma unroll
         for (int e = 0; e < V; ++e) v[e] = load_elem(p, dt, i + e);
@@ -111,28 +127,24 @@ __device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
 
 // One rounding to the stored type, nearest even.  STREAM: results that no
 // cache will hold until they are read (8 elements at a time only).
-template <int V, bool STREAM = false>
+template <int V, bool STREAM = false, bool ANY = false>
 __device__ __forceinline__ void store_f32(void* p, int dt, int64_t i, const float (&v)[V]) {
     if constexpr (V == 8) {
+        u32x4 u;
         if (dt == MOE_DT_F32) {
-            f32x4* q = reinterpret_cast<f32x4*>(static_cast<float*>(p) + i);
-            const f32x4 a = {v[0], v[1], v[2], v[3]}, b = {v[4], v[5], v[6], v[7]};
-            if constexpr (STREAM) {
-                __builtin_nontemporal_store(a, q);
-                __builtin_nontemporal_store(b, q + 1);
-            } else {
-                q[0] = a;
-                q[1] = b;
+            float* q = static_cast<float*>(p) + i;
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+#pragma unroll
+                for (int e = 0; e < 4; ++e) u[e] = __float_as_uint(v[4 * h + e]);
+                store16<STREAM, ANY>(q + 4 * h, u);
             }
         } else {
-            u32x4 u;
 #pragma unroll
             for (int e = 0; e < 4; ++e)
                 u[e] = dt == MOE_DT_BF16 ? pack_bf16(v[2 * e], v[2 * e + 1])
                                          : pack_f16(v[2 * e], v[2 * e + 1]);
-            u32x4* q = reinterpret_cast<u32x4*>(static_cast<uint16_t*>(p) + i);
-            if constexpr (STREAM) __builtin_nontemporal_store(u, q);
-            else *q = u;
+            store16<STREAM, ANY>(static_cast<uint16_t*>(p) + i, u);
         }
     } else {
 #pragma unroll
@@ -142,6 +154,21 @@ __device__ __forceinline__ void store_f32(void* p, int dt, int64_t i, const floa
             else
                 static_cast<uint16_t*>(p)[i + e] =
                     (uint16_t)(dt == MOE_DT_BF16 ? pack_bf16(v[e], 0.f) : pack_f16(v[e], 0.f));
+        }
+    }
+}
+
+// Elements lo .. V - 1 of a chunk (lo <= 0: all of it, at i and on).
+template <int V, bool STREAM, bool ANY>
+__device__ __forceinline__ void store_from(void* p, int dt, int64_t i, const float (&v)[V],
+                                           int lo) {
+    if (!ANY || lo <= 0) {
+        store_f32<V, STREAM, ANY>(p, dt, i, v);
+    } else {
+#pragma unroll
+        for (int e = 1; e < V; ++e) {
+            const float one[1] = {v[e]};
+            if (e >= lo) store_f32<1>(p, dt, i + e, one);
         }
     }
 }

@@ -6,7 +6,8 @@
 // registers (NCH chunks of V elements per thread) between its maximum and its
 // codes; rows past that (NCH = 0) are read a second time, from L2.  Bound by
 // HBM: 4096 x 6144 bf16 to codes, 75 MB, in 20 us; the fp32 middle rows of a
-// routed prefill batch (32768 x 2048), 336 MB, in 55 us.
+// routed prefill batch (32768 x 2048), 336 MB, in 55 us; 4096 x 6145, whose rows
+// start off 16 bytes, in 24 (39 element by element).
 #include <type_traits>
 
 #include "elem_dev.h"
@@ -23,31 +24,37 @@ struct QuantArgs {
     int dt, K, nw;   // nw: waves of a row
 };
 
+// Codes of elements lo .. V - 1 of a chunk at h (lo 0: all, on 8 bytes).
 template <int V>
-__device__ __forceinline__ void store_codes(int8_t* q, int h, const float (&v)[V], float mul) {
-    if constexpr (V == 8) {
-        const uint2 u = {pack_codes4(&v[0], mul), pack_codes4(&v[4], mul)};
+__device__ __forceinline__ void store_codes(int8_t* q, int h, const float (&v)[V], float mul,
+                                            int lo) {
+    if (V == 8 && lo == 0) {
+        const uint2 u = {pack_codes4(&v[0], mul), pack_codes4(&v[V / 2], mul)};
         *reinterpret_cast<uint2*>(q + h) = u;
     } else {
 #pragma unroll
-        for (int e = 0; e < V; ++e) q[h + e] = (int8_t)code_of(v[e], mul);
+        for (int e = 0; e < V; ++e)
+            if (e >= lo) q[h + e] = (int8_t)code_of(v[e], mul);
     }
 }
 
-template <int V, int NCH>
+// ANY: rows that start off 16 bytes or end inside a chunk; the last chunk then
+// ends at the row's end and shares `lo` elements with the one before.
+template <int V, int NCH, bool ANY>
 __global__ __launch_bounds__(1024) void k_quantize(QuantArgs A) {
     __shared__ uint32_t red[16];
     const int tid = threadIdx.x, nt = A.nw * 64;
     const int64_t t = A.t0 + blockIdx.x;
     int8_t* q = A.q + t * A.ldq;
     uint32_t amax = 0u;
+    auto at = [&](int h) { return ANY ? min(h, A.K - V) : h; };
     if constexpr (NCH > 0) {
         float v[NCH][V];
 #pragma unroll
         for (int c = 0; c < NCH; ++c) {
             const int h = (c * nt + tid) * V;
             if (h < A.K) {
-                load_f32<V>(A.x, A.dt, t * A.ldx + h, v[c]);
+                load_f32<V, ANY>(A.x, A.dt, t * A.ldx + at(h), v[c]);
             } else {
 #pragma unroll
                 for (int e = 0; e < V; ++e) v[c][e] = 0.f;
@@ -63,12 +70,12 @@ __global__ __launch_bounds__(1024) void k_quantize(QuantArgs A) {
 #pragma unroll
         for (int c = 0; c < NCH; ++c) {
             const int h = (c * nt + tid) * V;
-            if (h < A.K) store_codes<V>(q, h, v[c], rc.mul);
+            if (h < A.K) store_codes<V>(q, at(h), v[c], rc.mul, h - at(h));
         }
     } else {
         for (int h = tid * V; h < A.K; h += nt * V) {
             float v[V];
-            load_f32<V>(A.x, A.dt, t * A.ldx + h, v);
+            load_f32<V, ANY>(A.x, A.dt, t * A.ldx + at(h), v);
 #pragma unroll
             for (int e = 0; e < V; ++e) amax = max(amax, __float_as_uint(v[e]) & 0x7fffffffu);
         }
@@ -77,8 +84,8 @@ __global__ __launch_bounds__(1024) void k_quantize(QuantArgs A) {
         if (tid == 0) A.scale[t] = rc.scale;
         for (int h = tid * V; h < A.K; h += nt * V) {
             float v[V];
-            load_f32<V>(A.x, A.dt, t * A.ldx + h, v);
-            store_codes<V>(q, h, v, rc.mul);
+            load_f32<V, ANY>(A.x, A.dt, t * A.ldx + at(h), v);
+            store_codes<V>(q, at(h), v, rc.mul, h - at(h));
         }
     }
     const int pad = (A.K + kI8TileK - 1) / kI8TileK * kI8TileK - A.K;
@@ -108,7 +115,7 @@ __global__ __launch_bounds__(256) void k_pack_i8(const int8_t* __restrict__ src,
     *reinterpret_cast<u32x4*>(dst + ((g0 + g * step) * nkt + kt) * kI8TileBytes + lane * 16) = u;
 }
 
-template <int V>
+template <int V, bool ANY>
 void launch_q(QuantArgs A, hipStream_t s) {
     const int nch = (A.K + V - 1) / V;
     auto waves = [&](int per) { return (nch + 64 * per - 1) / (64 * per); };
@@ -118,13 +125,12 @@ void launch_q(QuantArgs A, hipStream_t s) {
         const int64_t most = rows_of_launch(A.nw);
         for (A.t0 = 0; A.t0 < A.T; A.t0 += most) {
             const int64_t n = A.T - A.t0 < most ? A.T - A.t0 : most;
-            k_quantize<V, NCH><<<(unsigned)n, A.nw * 64, 0, s>>>(A);
+            k_quantize<V, NCH, ANY><<<(unsigned)n, A.nw * 64, 0, s>>>(A);
         }
     };
-    constexpr int C0 = V == 8 ? 1 : 2, C1 = V == 8 ? 4 : 16;
-    if (waves(C0) <= 16) go(std::integral_constant<int, C0>{}, C0);
-    else if (waves(C1) <= 16) go(std::integral_constant<int, C1>{}, C1);
-    else go(std::integral_constant<int, 0>{}, 0);
+    if (V == 1 || waves(1) <= 16) go(std::integral_constant<int, 1>{}, 1);
+    else if (waves(4) <= 16) go(std::integral_constant<int, V == 8 ? 4 : 1>{}, 4);
+    else go(std::integral_constant<int, V == 8 ? 0 : 1>{}, 0);
 }
 
 }  // namespace
@@ -133,8 +139,9 @@ int launch_quantize_i8(const void* x, int dt, int64_t ldx, int64_t T, int32_t K,
                        int64_t ldq, float* scale, bool vec8, void* stream) {
     hipStream_t s = reinterpret_cast<hipStream_t>(stream);
     QuantArgs A{x, ldx, ldq, T, 0, q, scale, dt, K, 1};
-    if (vec8) launch_q<8>(A, s);
-    else launch_q<1>(A, s);
+    if (vec8) launch_q<8, false>(A, s);
+    else if (K >= 8) launch_q<8, true>(A, s);
+    else launch_q<1, false>(A, s);
     MOEQ_CHECK_LAUNCH();
     return MOE_OK;
 }

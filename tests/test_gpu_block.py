@@ -176,6 +176,54 @@ def test_rows_do_not_depend_on_the_batch():
             assert torch.equal(a[0], b[t])
 
 
+@pytest.mark.parametrize("dt", sorted(TYPES))
+@pytest.mark.parametrize("T,H,off", [(3, 8, 1), (5, 256, 3), (2100, 1024, 1), (2, 9000, 5)])
+def test_bits_do_not_follow_the_alignment(T, H, off, dt):
+    """Rows at an element's alignment give the bits of the same rows on 16 bytes,
+    also where the results go over the operands."""
+    rs = np.random.default_rng(H + off)
+    k = 2
+    r, y = rnd(rs, (T, H), TYPES[dt]), rnd(rs, (T * k, H), TYPES[dt])
+    w, tw = rnd(rs, (H,), TYPES[dt]), rnd(rs, (T, k), torch.float32)
+    inv = torch.arange(T * k, dtype=torch.int32, device=DEV).flip(0).contiguous()
+    wide = torch.full((T, H + off + 2), 7.0, dtype=TYPES[dt], device=DEV)
+    at = wide[:, off:off + H]
+    ref = moeq.block_residual(r, y[:T], w, post_w=w, codes=True)
+    at.copy_(r)
+    got = moeq.block_residual(at, y[:T], w, post_w=w, r_out=at, codes=True)
+    for a, b in zip(got, ref):
+        assert torch.equal(a, b)
+    ref = moeq.combine_residual(r, y, inv, tw, w, codes=True)
+    at.copy_(r)
+    got = moeq.combine_residual(at, y, inv, tw, w, r_out=at, codes=True)
+    for a, b in zip(got, ref):
+        assert torch.equal(a, b)
+    at.copy_(r)
+    for a, b in zip(moeq.quantize_i8(at), moeq.quantize_i8(r)):
+        assert torch.equal(a, b)
+    assert torch.all(wide[:, :off] == 7) and torch.all(wide[:, off + H:] == 7)
+
+
+@pytest.mark.parametrize("H", [7, 8, 9, 15, 511, 513, 1003, 8191, 8193, 16391, 32767])
+def test_odd_rows_in_place(H):
+    """The last chunk of a row shares elements with the one before: results over
+    the operands are those beside them."""
+    rs = np.random.default_rng(H)
+    for T in (3, 700):
+        r, y, w = rnd(rs, (T, H), torch.bfloat16), rnd(rs, (T, H), torch.bfloat16), \
+            rnd(rs, (H,), torch.bfloat16)
+        ref_r, ref_n = moeq.block_residual(r, y, w, post_w=w, gate=y)
+        n2 = y.clone()
+        r2 = r.clone()
+        moeq.block_residual(r2, n2, w, post_w=w, gate=y, r_out=r2)
+        assert torch.equal(r2, ref_r)
+        moeq.block_norm(r2, w, out=r2)
+        assert torch.equal(r2, moeq.block_norm(ref_r, w))
+        want = ob.block(f64(r), f64(y), f64(w), f64(w), f64(y))
+        close(ref_r, want[0], want[1], "r'")
+        close(ref_n, want[2], want[3], "n")
+
+
 def test_more_rows_than_one_launch_holds():
     """A launch ends at 2^32 threads, 2^26 rows of one wave each: the rows behind
     it, and those beside the border, are done all the same."""
