@@ -682,10 +682,10 @@ int moe_shared_ffn_i8(const moe_i8_layer* shared, const void* x, int32_t x_dtype
  *             as moe_quantize_i8 writes it.  Outputs that are NULL are not
  *             written; at least one is given.
  *   All pointers [device]; float operands are F32, BF16 or F16, post_w and
- *   pre_w [H] of w_dtype.  Rows whose starts and strides are multiples of 16
- *   bytes (and H of 8) take vector loads, others scalar ones.
+ *   pre_w [H] of w_dtype, at any alignment of their elements (rows on 16 bytes
+ *   with H a multiple of 8 are fastest).
  *   Limits: 1 <= H <= MOE_BLOCK_MAX_H, 0 <= k <= MOE_MAX_K, eps >= 0.
- *   The bits do not depend on T, and are the same run to run.
+ *   A row's bits depend on neither T nor alignment, and are the same run to run.
  */
 typedef struct moe_block {
     const void* y;            int64_t ld_y;
