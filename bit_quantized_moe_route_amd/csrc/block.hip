@@ -252,7 +252,7 @@ __global__ __launch_bounds__(1024) void k_block(BlockRow A) {
         } else {
 #pragma unroll
             for (int e = 0; e < V; ++e)
-                if (e >= lo(c)) q[at(c) + e] = (int8_t)code_of(v[c][e], rc.mul);
+                if (e >= lo(c)) q[at(c) + e] = code1(v[c][e], rc.mul);
         }
     }
     const int pad = (H + 63) / 64 * 64 - H;

@@ -94,7 +94,7 @@ __device__ __forceinline__ void code_row(const I8Pass& A, int64_t src, int8_t* q
             *reinterpret_cast<uint2*>(q + h) =
                 uint2{pack_codes4(v, rc.mul), pack_codes4(v + 4, rc.mul)};
         else
-            q[h] = (int8_t)code_of(v[0], rc.mul);
+            q[h] = code1(v[0], rc.mul);
     });
     for (int h = A.K + tid; h < width; h += KS * 64) q[h] = 0;
     if constexpr (KS > 1) __syncthreads();   // red is free again

@@ -2,12 +2,12 @@
 // weight matrices.
 //
 // Row t of x [T, K]:  a = max_k |x[t, k]|,  scale[t] = a / 127,
-// q[t, k] = rint(x[t, k] * (127 / a)).  One pass over x: a row stays in
+// q[t, k] = rint(127 x[t, k] / a).  One pass over x: a row stays in
 // registers (NCH chunks of V elements per thread) between its maximum and its
 // codes; rows past that (NCH = 0) are read a second time, from L2.  Bound by
-// HBM: 4096 x 6144 bf16 to codes, 75 MB, in 20 us; the fp32 middle rows of a
-// routed prefill batch (32768 x 2048), 336 MB, in 55 us; 4096 x 6145, whose rows
-// start off 16 bytes, in 24 (39 element by element).
+// HBM: 4096 x 6144 bf16 to codes, 75 MB, in 22 us; the fp32 middle rows of a
+// routed prefill batch (32768 x 2048), 336 MB, in 57 us; 4096 x 6145, whose rows
+// start off 16 bytes, in 25 (39 element by element).
 #include <type_traits>
 
 #include "elem_dev.h"
@@ -26,7 +26,7 @@ struct QuantArgs {
 
 // Codes of elements lo .. V - 1 of a chunk at h (lo 0: all, on 8 bytes).
 template <int V>
-__device__ __forceinline__ void store_codes(int8_t* q, int h, const float (&v)[V], float mul,
+__device__ __forceinline__ void store_codes(int8_t* q, int h, const float (&v)[V], double mul,
                                             int lo) {
     if (V == 8 && lo == 0) {
         const uint2 u = {pack_codes4(&v[0], mul), pack_codes4(&v[V / 2], mul)};
@@ -34,7 +34,7 @@ __device__ __forceinline__ void store_codes(int8_t* q, int h, const float (&v)[V
     } else {
 #pragma unroll
         for (int e = 0; e < V; ++e)
-            if (e >= lo) q[h + e] = (int8_t)code_of(v[e], mul);
+            if (e >= lo) q[h + e] = code1(v[e], mul);
     }
 }
 
