@@ -196,7 +196,7 @@ __global__ __launch_bounds__(KS * 64) void k_i8(I8Pass A, int ngroups, bool quad
                 for (int i = 0; i < 4; ++i) acc[g][i] = sums[(g * 4 + i) * 64 + lane];
         }
         if (in) {
-            const float sq = XR ? xscale[lane & 15] : A.qscale[src];
+            const Scale sq = split(XR ? xscale[lane & 15] : A.qscale[src]);
 #pragma unroll
             for (int g = 0; g < NG; g += PAIR ? 2 : 1) {
                 // one wave writes a row group
@@ -207,10 +207,10 @@ __global__ __launch_bounds__(KS * 64) void k_i8(I8Pass A, int ngroups, bool quad
                 for (int i = 0; i < 4; ++i) {
                     const int c = min(ch + i, A.N - 1);
                     if constexpr (PAIR)
-                        y[i] = silu_mul(sq * sw[c] * (float)acc[g][i],
-                                        sq * sw[A.N + c] * (float)acc[g + 1][i]);
+                        y[i] = silu_mul(scaled(sq, split(sw[c]), acc[g][i]),
+                                        scaled(sq, split(sw[A.N + c]), acc[g + 1][i]));
                     else
-                        y[i] = sq * sw[c] * (float)acc[g][i] + (A.bias ? A.bias[c] : 0.f);
+                        y[i] = scaled(sq, split(sw[c]), acc[g][i]) + (A.bias ? A.bias[c] : 0.f);
                 }
                 const int64_t at = row * A.ld_out + ch;
                 if (quads) {

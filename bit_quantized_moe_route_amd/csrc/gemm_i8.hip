@@ -290,34 +290,34 @@ __global__ __launch_bounds__(64 * CW * KP, 2) void k_gemm_i8(I8Pass A, int ngrou
                     if (row >= left) continue;
                     if constexpr (KP > 1) {
                         const int32_t* own = sums + wave * (BM * 64) + lane;
-                        f(qs[row], own[(i * 32 + v) * 64], own[(i * 32 + 16 + v) * 64],
+                        f(split(qs[row]), own[(i * 32 + v) * 64], own[(i * 32 + 16 + v) * 64],
                           (first + row) * A.ld_out);
                     } else {
-                        f(qs[row], acc[i][0][v], acc[i][1][v], (first + row) * A.ld_out);
+                        f(split(qs[row]), acc[i][0][v], acc[i][1][v], (first + row) * A.ld_out);
                     }
                 }
         };
         if constexpr (PAIR) {
             const int ch = g0 * 8 + col;
             if (ch >= A.N) return;
-            const float sg = sw[ch], su = sw[A.N + ch];
+            const Scale sg = split(sw[ch]), su = split(sw[A.N + ch]);
             float* h = static_cast<float*>(A.out) + ch;
-            rows([&](float q, int g, int u, int64_t at) {
-                h[at] = silu_mul(q * sg * (float)g, q * su * (float)u);
+            rows([&](Scale q, int g, int u, int64_t at) {
+                h[at] = silu_mul(scaled(q, sg, g), scaled(q, su, u));
             });
         } else {
             const int ch = g0 * 16 + 2 * col;
             if (ch >= A.N) return;
             const bool two = ch + 1 < A.N;
-            const float s0 = sw[ch], s1 = two ? sw[ch + 1] : 0.f;
+            const Scale s0 = split(sw[ch]), s1 = split(two ? sw[ch + 1] : 0.f);
             const float b0 = A.bias ? A.bias[ch] : 0.f, b1 = A.bias && two ? A.bias[ch + 1] : 0.f;
             auto store = [&](auto zero) {
                 using T = decltype(zero);
                 typedef T T2 __attribute__((ext_vector_type(2)));
                 T* o = static_cast<T*>(A.out) + ch;
-                rows([&](float q, int a0, int a1, int64_t at) {
-                    const T y0 = as_type<T>(q * s0 * (float)a0 + b0);
-                    const T y1 = as_type<T>(q * s1 * (float)a1 + b1);
+                rows([&](Scale q, int a0, int a1, int64_t at) {
+                    const T y0 = as_type<T>(scaled(q, s0, a0) + b0);
+                    const T y1 = as_type<T>(scaled(q, s1, a1) + b1);
                     if (pairs) {
                         *reinterpret_cast<T2*>(o + at) = T2{y0, y1};
                     } else {

@@ -33,6 +33,21 @@ __device__ __forceinline__ float silu_mul(float g, float u) {
     return g * __builtin_amdgcn_rcpf(1.f + __expf(-g)) * u;
 }
 
+// A scale as mant * 2^exp, |mant| in [1/2, 1): the product of a row's and a
+// channel's scale may leave fp32's normal range where the result does not.
+struct Scale {
+    float mant;
+    int exp;
+};
+__device__ __forceinline__ Scale split(float s) {
+    return Scale{__builtin_amdgcn_frexp_mantf(s), __builtin_amdgcn_frexp_expf(s)};
+}
+// a * b * sum.  The powers of two are exact: the bits are those of the three
+// factors' product in fp32 wherever that stays in range.
+__device__ __forceinline__ float scaled(Scale a, Scale b, int32_t sum) {
+    return __builtin_ldexpf(a.mant * b.mant * (float)sum, a.exp + b.exp);
+}
+
 // y as T.  An fp16 is rounded from the fp32 value like everywhere else: folded
 // into one instruction with the sum that makes y, it would be rounded once where
 // the other kernels round twice, and a row's bits would follow the kernel.

@@ -603,7 +603,7 @@ typedef struct moe_i8_linear {
 /*
  * moe_linear_i8 -- out[t, n] = x_scale[t] * w_scale[n] * sum_k q[t, k] W[n, k]
  * (+ bias[n]): the sum exact in int32, the rest in fp32, rounded once to
- * out_dtype.
+ * out_dtype.  The scales' own product may lie outside fp32's range.
  *   x          [device] codes (x_dtype MOE_DT_I8, rows as moe_quantize_i8
  *              writes them, with x_scale [T]), or [T, K] of a float type,
  *              which the call codes as moe_quantize_i8 does (x_scale NULL).
