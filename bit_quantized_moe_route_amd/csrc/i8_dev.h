@@ -27,10 +27,12 @@ __device__ __forceinline__ void keep_order() {
 // around matrix instructions go by, which run whatever the lane mask says.
 __device__ __forceinline__ int uniform(int v) { return __builtin_amdgcn_readfirstlane(v); }
 
-// silu(g) * u.  The exponential and the reciprocal are the hardware's (each
-// within an ulp or two of fp32), far inside what the 8-bit code of h resolves.
+// silu(g) * u to a few ulps of fp32 (g > -87; below, exp(-|g|) is subnormal):
+// the exponential within an ulp, and neither it nor the quotient overflows.  (The
+// hardware's exponential rounds its argument first and is off by |g| 2^-24.)
 __device__ __forceinline__ float silu_mul(float g, float u) {
-    return g * __builtin_amdgcn_rcpf(1.f + __expf(-g)) * u;
+    const float e = expf(-fabsf(g));
+    return (g < 0.f ? e == 0.f ? 0.f : g * e : g) / (1.f + e) * u;
 }
 
 // A scale as mant * 2^exp, |mant| in [1/2, 1): the product of a row's and a
