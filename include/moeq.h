@@ -669,7 +669,8 @@ int moe_shared_ffn_i8(const moe_i8_layer* shared, const void* x, int32_t x_dtype
  *   r' = r_scale * r + y_scale * gate * p
  *   n  = pre_w ? N(r'; pre_w) : r'
  *   N(v; w) = v / sqrt(mean(v^2) + eps) * (w_offset + w)
- * n is taken from r' before r' is rounded to r_out.
+ * n is taken from r' before r' is rounded to r_out.  N is that of every finite
+ * row, also where v^2 leaves fp32's range; a row of zeros with eps 0 is NaN.
  *
  *   y         [T, H] (k == 0), [T*k, H] (k > 0) or NULL (then r' = r_scale r:
  *             the norm before a block alone).
