@@ -281,6 +281,8 @@ def combine_residual(r, y_perm, inv_perm, topk_w, w=None, *, y_shared=None, shar
     shared_gate fp32 [T] (1 if not given).  r None: no residual stream, r' is
     the gated sum itself (fp32, or of r_out's type)."""
     torch = _torch()
+    if topk_w.dim() != 2 or topk_w.shape[1] < 1:
+        raise ValueError(f"topk_w must be [T, k] with k at least 1, got {list(topk_w.shape)}")
     dev = _cuda(y_perm, "combine_residual")
     T, k = topk_w.shape
     H = y_perm.shape[1]
