@@ -13,10 +13,10 @@
 // per thread), so every operand is read once and every result written once; the
 // reductions (b^2, r'^2, max |n|) go through LDS.  HBM bounds large batches: at
 // 4096 tokens, H 6144, bf16, rows that no cache holds, the norm alone moves 101
-// MB in 22 us, norm after + gate + residual + norm before 201 MB in 47 us, the
-// gated sum of 8 rows + residual + norm 554 MB in 103 us (4.6, 4.3 and 5.4 TB/s;
+// MB in 25 us, norm after + gate + residual + norm before 201 MB in 47 us, the
+// gated sum of 8 rows + residual + norm 554 MB in 106 us (4.0, 4.3 and 5.2 TB/s;
 // a plain copy reaches 4.8).  Small ones are bound by a launch and two or three
-// dependent steps: 3.2 us for one token's norm, 6.2 for its gated sum.
+// dependent steps: 3.2 us for one token's norm, 6.7 for the gated sum of 8 tokens.
 #include <type_traits>
 
 #include "elem_dev.h"

@@ -11,10 +11,14 @@
 //
 // The weights' stream bounds it.  Measured (us, weights from HBM): routed
 // experts, H 6144, I 2048, 8 of 256, gate/up + codes of h + down: 58 at one
-// token (302 MB), 337 at 8, 928 at 32 (6.2 GB: 6.6 TB/s, a read alone reaches
-// 6.1 to 7.0).  One 6144 x 6144 matrix at one token 9.8 (38 MB), 1024 x 1024 3.5.
-// Many experts stream best from one-wave workgroups (KS 1, 8 tiles in flight:
-// 889 us at 32 tokens against 951 with 2 x 2 waves, 967 with KS 4); a lone
+// token (302 MB), 340 at 8, 926 at 32 (167 experts, 6.3 GB: 6.8 TB/s, a read alone
+// reaches 6.1 to 7.0).  A skewed router costs more: an expert's workgroups stream
+// its weights once for every 16 rows, one time after the other (tokens by a Zipf
+// law over the experts, at 32 / 64 / 128 / 256 tokens: 615 / 989 / 1369 / 1916 us,
+// 1.09 / 1.12 / 1.23 / 1.50 times the touched weights at 7.0 TB/s).
+// One 6144 x 6144 matrix at one token 10.2 (38 MB), 1024 x 1024 3.5.
+// Many experts stream best from one-wave workgroups (KS 1, 8 tiles in flight: on
+// one routing of 32 tokens 889 us, 951 with 2 x 2 waves, 967 with KS 4); a lone
 // matrix needs its inputs split to fill the chip (KS 4 with 2 row groups, 8 with
 // one below 256 row groups: 6144 -> 2048 5.9 us against 8.2 with KS 4).
 #include <type_traits>
