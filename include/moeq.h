@@ -559,7 +559,7 @@ int moe_layer_forward_shared(const moe_qlayer* layer, const moe_qlayer* shared,
 /*
  * moe_quantize_i8 -- the 8-bit code of every row of x:
  *   a = max_k |x[t, k]|,  scale[t] = a / 127,
- *   q[t, k] = rint(127 * x[t, k] / a)      (of the exact quotient, ties to even)
+ *   q[t, k] = rint(127 * x[t, k] / a)      (the exact quotient, ties to even; |q| <= 127)
  *   A row whose a is below 127 * 2^-126 gets scale 0 and codes 0; a row that
  *   holds an infinity or a NaN gets scale NaN and codes 0, so that every
  *   product of that row is NaN and no other row is touched.
