@@ -18,6 +18,10 @@ Calls (same names as the C ABI in include/moeq.h):
         stream before and after a block (block.py)
     quantize_i8, linear_i8, expert_ffn_i8, shared_ffn_i8, forward_i8 -- products
         in 8-bit integers (I8Linear, I8Layer; block.py)
+    add_adapters -- low-rank adapters of many requests beside a projection
+        (Adapters, adapter_plan; adapters.py)
+    head_norm_rope, token_logprobs -- norms and rotation of query and key heads,
+        log probabilities of given tokens (rope_table; heads.py)
 Host packers: quantize_nvfp4, quantize_nvfp4_residual, pack_nvfp4_expert,
 pack_nvfp4r_expert, pack_vq_expert, pack_vq8_expert, pack_bf16_expert,
 record_bytes, record_table.  Test hook: dequant_q.
@@ -918,4 +922,12 @@ from .block import (DT_BF16, DT_F16, DT_F32, DT_I8, I8Layer, I8Linear, block_nor
                     ffn_i8_workspace, forward_i8, linear_i8, linear_i8_workspace, quantize_i8,
                     shared_ffn_i8)
 
-_PROTOS.update(_block_calls.PROTOS)
+from . import adapters as _adapter_calls, heads as _head_calls  # noqa: E402
+from .adapters import (AdapterPlan, Adapters, adapter_plan, add_adapters,  # noqa: E402,F401
+                       add_adapters_workspace)
+from .heads import (head_norm_rope, rope_table, token_logprobs,  # noqa: E402,F401
+                    token_logprobs_workspace)
+
+for _calls in (_block_calls, _adapter_calls, _head_calls):
+    _PROTOS.update(_calls.PROTOS)
+    _block_calls.NAMES.update(_calls.PROTOS)

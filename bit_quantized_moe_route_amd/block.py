@@ -120,6 +120,7 @@ def _cuda(t, name):
 
 
 _fns = {}
+NAMES = set()       # the functions that _call looks up: block.py's, adapters.py's, heads.py's
 
 
 def _bind(L):
@@ -128,7 +129,7 @@ def _bind(L):
     replaced whole: another thread's call keeps the one it looked up."""
     global _fns
     torch = _torch()
-    f = {n: getattr(L, n) for n in PROTOS}
+    f = {n: getattr(L, n) for n in NAMES}
     f["lib"] = L
     f["stream"] = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
         lambda i: torch.cuda.current_stream(i).cuda_stream)

@@ -4,46 +4,14 @@
 #include <cstdint>
 #include <string>
 
-#include "internal.h"
+#include "api_checks.h"
 
 using namespace moeq;
 
 namespace {
 
-constexpr size_t kAlign = 256;
-constexpr int64_t kMaxRows = (int64_t)1 << 31;   // grid rows of one launch
 constexpr int32_t kMaxI8K = 131071;   // 2^31 / (128 * 128): int32 sums cannot wrap
 constexpr int32_t kMaxDim = 1 << 24;
-
-size_t align_up(size_t v) { return (v + kAlign - 1) / kAlign * kAlign; }
-
-bool float_dt(int dt) { return dt == MOE_DT_F32 || dt == MOE_DT_BF16 || dt == MOE_DT_F16; }
-int64_t dt_bytes(int dt) { return dt == MOE_DT_F32 ? 4 : dt == MOE_DT_I8 ? 1 : 2; }
-
-bool aligned(const void* p, uintptr_t n) { return reinterpret_cast<uintptr_t>(p) % n == 0; }
-
-int bad(const std::string& fn, const char* what) { return fail(MOE_EINVAL, fn + ": " + what); }
-
-// Operand rows of H elements: the type, the pointer's natural alignment and
-// the row stride; vec8 is cleared if a row may start off a 16-byte border.
-int check_rows(const std::string& fn, const char* name, const void* p, int dt, int64_t ld,
-               int64_t H, bool& vec8) {
-    if (!float_dt(dt))
-        return fail(MOE_EUNSUPPORTED, fn + ": " + name + " has an unknown element type");
-    if (!aligned(p, (uintptr_t)dt_bytes(dt)))
-        return fail(MOE_EINVAL, fn + ": " + name + " is not aligned to its element type");
-    if (ld < H) return fail(MOE_EINVAL, fn + ": the row stride of " + name + " is below the width");
-    vec8 = vec8 && aligned(p, 16) && ld * dt_bytes(dt) % 16 == 0;
-    return MOE_OK;
-}
-
-int check_codes(const std::string& fn, const char* name, const void* q, int64_t ldq, int64_t K) {
-    if (!aligned(q, 16) || ldq % 16 || ldq < round_up(K, kI8TileK))
-        return fail(MOE_EINVAL, fn + ": " + name +
-                                    " needs 16-byte aligned rows of at least the width rounded up "
-                                    "to 64 codes");
-    return MOE_OK;
-}
 
 // The products' tiles are 128 rows by 256 channels wherever they are many, and
 // no smaller than 32 rows for up to 64 rows of each expert: the workgroups of a

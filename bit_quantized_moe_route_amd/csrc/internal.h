@@ -255,6 +255,55 @@ struct I8Pass {
 bool i8_codes_itself(int64_t T, int32_t K, bool routed);
 int launch_i8(const I8Pass& p, bool pair, void* stream);
 int launch_gemm_i8(const I8Pass& p, bool pair, void* stream);
+// Norm and rotation of query and key heads.
+int launch_heads(const moe_heads& h, int64_t T, void* stream);
+// Log probabilities of rows of logits: slices of a row, at most kLogprobSlices of
+// them; ws: 16 + 8 top bytes a slice.
+constexpr int kLogprobSlice = 16384, kLogprobSlices = 64;
+int launch_logprobs(const moe_logprobs& P, int64_t T, void* ws, void* stream);
+// Low-rank adapters.  A's tiles: 16 ranks x 32 inputs, 1 KB in the order of the
+// matrix instruction's operand (lane L: rank L & 15, inputs (L >> 4) * 8 + 0..7), by
+// adapter, rank tile, input tile; the inputs padded with zeros to whole chains.
+// B's: 16 channels x 16 ranks, 512 bytes (lane L of 32: row L & 15, ranks (L >> 4) * 8
+// + 0..7), by adapter, group of 64 channels, rank tile, row tile j of 4; row r of tile
+// j is channel (j >> 1) * 32 + (r >> 2) * 8 + (j & 1) * 4 + (r & 3) of the group, so
+// that a lane's results are 8 neighbouring channels, twice.
+constexpr int kAdChain = 128;                  // inputs summed in one go
+constexpr int kAdTile = 16;                    // tokens of a tile
+inline int64_t ad_rank_tiles(int32_t rank) { return round_up(rank, 16) / 16; }
+inline int64_t ad_a_bytes(int32_t rank, int32_t K) {
+    return ad_rank_tiles(rank) * (round_up(K, kAdChain) / 32) * 1024;
+}
+inline int64_t ad_b_bytes(int32_t rank, int32_t N) {
+    return round_up(N, 64) / 64 * ad_rank_tiles(rank) * 2048;
+}
+// What a plan holds, in int32 from its start: the tokens by adapter (those without
+// one last), tiles of one adapter each (adapter, first, tokens, 0), and the sort's
+// own arrays.  max_tiles bounds the tiles' number, which is at 0.
+struct AdPlan {
+    int64_t order, tiles, ids, counts, offsets, inv, ws, total;
+    int64_t max_tiles;
+};
+inline AdPlan ad_plan(int64_t T, int32_t n) {
+    AdPlan p;
+    p.max_tiles = T / kAdTile + (T < n + 1 ? T : n + 1);
+    p.order = 4;
+    p.tiles = p.order + round_up(T, 4);
+    p.ids = p.tiles + 4 * p.max_tiles;
+    p.counts = p.ids + round_up(T, 4);
+    p.offsets = p.counts + round_up(n + 1, 4);
+    p.inv = p.offsets + round_up(n + 2, 4);
+    p.ws = p.inv + round_up(T, 4);
+    p.total = p.ws + (int64_t)permute_ws_bytes(T, 1, n + 1) / 4;
+    return p;
+}
+int launch_adapter_plan(const int32_t* ids, int64_t T, int32_t n, int32_t* plan, void* stream);
+int launch_pack_adapter(const moe_adapters& S, int32_t slot, const void* a, int64_t lda,
+                        const void* b, int64_t ldb, int32_t rank, float scale, void* stream);
+int launch_add_adapters(const moe_adapters& S, const void* x, int32_t x_dtype, int64_t ldx,
+                        const float* x_scale, const int32_t* plan, int64_t T, const void* y,
+                        void* out, int32_t y_dtype, int64_t ldy, int64_t ldo, float* h,
+                        void* stream);
 int launch_probe_read(const void* buf, size_t bytes, uint32_t* sink, int blocks, void* stream);
 
 }  // namespace moeq

@@ -257,6 +257,71 @@ __global__ __launch_bounds__(64 * kSmallMaxWaves) void k_route_permute_small(
     }
 }
 
+// ---------------------------------------------------------------- adapter plans
+// The tokens of a batch sorted by the adapter of their request (an id outside [0, n)
+// is none, bin n), and tiles of up to kAdTile tokens of one adapter.
+__device__ __forceinline__ int adapter_bin(int id, int n) { return id >= 0 && id < n ? id : n; }
+
+// The tile list from each bin's count and first slot (threads tid < E hold bin tid's).
+// base, first, number: LDS [kPermThreads].
+__device__ __forceinline__ void write_tiles(int count, int first, int E, int* base, int* firsts,
+                                            int* counts, int* wtot, int32_t* plan, int64_t tiles) {
+    const int tid = threadIdx.x;
+    const int mine = tid < E ? (count + kAdTile - 1) / kAdTile : 0;
+    const int at = block_exclusive_scan(mine, wtot);
+    base[tid] = at;
+    firsts[tid] = first;
+    counts[tid] = count;
+    if (tid == E - 1) plan[0] = at + mine;
+    __syncthreads();
+    const int total = base[E - 1] + (counts[E - 1] + kAdTile - 1) / kAdTile;
+    for (int i = tid; i < total; i += kPermThreads) {
+        int lo = 0, hi = E;                       // base[lo] <= i < base[hi]
+        while (hi - lo > 1) {
+            const int mid = (lo + hi) / 2;
+            if (base[mid] <= i) lo = mid;
+            else hi = mid;
+        }
+        const int skip = (i - base[lo]) * kAdTile;
+        int32_t* t = plan + tiles + 4 * (int64_t)i;
+        t[0] = lo;
+        t[1] = firsts[lo] + skip;
+        t[2] = min(counts[lo] - skip, kAdTile);
+        t[3] = 0;
+    }
+}
+
+constexpr int kPlanSingle = 4096;                 // tokens of a plan in one launch
+
+__global__ __launch_bounds__(kPermThreads) void k_plan(const int32_t* __restrict__ ids, int T,
+                                                       int n, int32_t* plan, AdPlan L) {
+    extern __shared__ int smem[];
+    __shared__ int sids[kPlanSingle];
+    __shared__ int base[kPermThreads], firsts[kPermThreads], number[kPermThreads];
+    const int tid = threadIdx.x, E = n + 1;
+    for (int t = tid; t < T; t += kPermThreads) sids[t] = adapter_bin(ids[t], n);
+    __syncthreads();
+    permute_body(sids, T, E, plan + L.counts, plan + L.offsets, plan + L.order, plan + L.inv, smem);
+    const int c = tid < E ? smem[tid] : 0;        // the histogram, and the bins' ends
+    const int end = tid < E ? smem[E + tid] : 0;
+    write_tiles(c, end - c, E, base, firsts, number, smem + 2 * E, plan, L.tiles);
+}
+
+__global__ __launch_bounds__(256) void k_adapter_bins(const int32_t* __restrict__ ids, int64_t T,
+                                                      int n, int32_t* __restrict__ bins) {
+    const int64_t t = (int64_t)blockIdx.x * 256 + threadIdx.x;
+    if (t < T) bins[t] = adapter_bin(ids[t], n);
+}
+
+__global__ __launch_bounds__(kPermThreads) void k_plan_tiles(int n, int32_t* plan, AdPlan L) {
+    __shared__ int base[kPermThreads], firsts[kPermThreads], number[kPermThreads];
+    __shared__ int wtot[kPermWaves];
+    const int tid = threadIdx.x, E = n + 1;
+    const int c = tid < E ? plan[L.counts + tid] : 0;
+    const int f = tid < E ? plan[L.offsets + tid] : 0;
+    write_tiles(c, f, E, base, firsts, number, wtot, plan, L.tiles);
+}
+
 }  // namespace
 
 // Slices of the large-batch path: at least kPermSlice assignments each, at
@@ -301,6 +366,24 @@ int launch_permute(const int32_t* ids, int64_t T, int32_t k, int32_t E, int32_t*
     const size_t lds = (size_t)(E + kPermWaves) * sizeof(int) + (size_t)kPermWaves * E;
     k_perm_scatter<<<nb, kPermThreads, lds, s>>>(ids, n, E, C, nb, hist, counts, offsets,
                                                  perm_src, inv_perm);
+    MOEQ_CHECK_LAUNCH();
+    return MOE_OK;
+}
+
+int launch_adapter_plan(const int32_t* ids, int64_t T, int32_t n, int32_t* plan, void* stream) {
+    hipStream_t s = reinterpret_cast<hipStream_t>(stream);
+    const AdPlan L = ad_plan(T, n);
+    if (T <= kPlanSingle) {
+        k_plan<<<1, kPermThreads, permute_lds_bytes(n + 1), s>>>(ids, (int)T, n, plan, L);
+        MOEQ_CHECK_LAUNCH();
+        return MOE_OK;
+    }
+    k_adapter_bins<<<(unsigned)((T + 255) / 256), 256, 0, s>>>(ids, T, n, plan + L.ids);
+    MOEQ_CHECK_LAUNCH();
+    const int st = launch_permute(plan + L.ids, T, 1, n + 1, plan + L.counts, plan + L.offsets,
+                                  plan + L.order, plan + L.inv, plan + L.ws, stream);
+    if (st) return st;
+    k_plan_tiles<<<1, kPermThreads, 0, s>>>(n, plan, L);
     MOEQ_CHECK_LAUNCH();
     return MOE_OK;
 }

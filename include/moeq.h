@@ -29,6 +29,13 @@
  *   moe_expert_ffn_i8   the routed experts' FFN, rows as moe_expert_ffn_q's
  *   moe_shared_ffn_i8   one expert on every token
  *
+ * and beside and behind a projection,
+ *
+ *   moe_add_adapters    low-rank adapters of many requests (moe_pack_adapter,
+ *                       moe_adapter_plan)
+ *   moe_head_norm_rope  norms and rotation of query and key heads
+ *   moe_token_logprobs  log probabilities of given tokens, entropy, best tokens
+ *
  * Passages these calls follow (titles and sections of the source pages):
  *   - 256 routed experts per MoE layer, 8 active per token:
  *     "GLM-5-NVFP4-MTP", Model Description.
@@ -708,6 +715,150 @@ typedef struct moe_block {
 } moe_block;
 
 int moe_block_norm(const moe_block* block, int64_t T, int32_t H, void* stream);
+
+/* ------------------------------------------ norms and rotation of query and key heads */
+
+#define MOE_HEAD_MAX_D 1024
+
+/* A set of heads: element d of head h of token t at x + t * ld_t + h * ld_h + d. */
+typedef struct moe_head_set {
+    const void* x;     int64_t ld_t, ld_h;            /* [device] */
+    void* out;         int64_t ld_out_t, ld_out_h;    /* [device]; may be x itself */
+    const void* w;                                    /* [device] [D] of w_dtype, or NULL: no norm */
+    int32_t heads, reserved;
+} moe_head_set;
+
+/*
+ * moe_head_norm_rope -- the norm of each query and key head and its rotation by the
+ * token's position, in one pass, all in fp32 with one rounding to dtype:
+ *   n = w ? v / sqrt(mean(v^2) + eps) * (w_offset + w) : v      over the D elements
+ *   (a, b) = pair i of n's first R elements: elements i and R/2 + i, or with
+ *            interleaved 2i and 2i + 1;  (c, s) = table[pos[t]][i], table[pos[t]][R/2 + i]
+ *   out = (a c - b s, b c + a s), n's other elements as they are
+ * The norm is that of every finite head, also where v^2 leaves fp32's range; a head of
+ * zeros with eps 0 is NaN.
+ *   q, k     k.heads 0: queries alone (or any one set).  Heads and tokens may lie
+ *            anywhere (parts of a wider projection); out is x with the same strides, or
+ *            overlaps no operand.
+ *   pos      [device] int32 or int64 (pos_bits 32, 64) [T], or NULL: no rotation.  A
+ *            position outside [0, table_rows) makes the rotated elements NaN.
+ *   table    [device] fp32 [table_rows, R]: R/2 cosines, then R/2 sines.
+ *   Limits: 1 <= D <= MOE_HEAD_MAX_D, R even in [2, D] with pos, up to 4096 heads a set,
+ *   x and out of dtype (F32, BF16, F16) at any alignment of their elements.  (D and R
+ *   multiples of 16 are fastest.)  A head's bits depend on neither T nor its neighbours.
+ */
+typedef struct moe_heads {
+    moe_head_set q, k;
+    const void* pos;
+    const float* table;
+    int64_t table_rows;
+    int32_t D, R, interleaved, pos_bits, dtype, w_dtype;
+    float eps, w_offset;
+} moe_heads;
+
+int moe_head_norm_rope(const moe_heads* heads, int64_t T, void* stream);
+
+/* ------------------------------------------------------- token log probabilities */
+
+#define MOE_MAX_TOP   32         /* best tokens of a row */
+#define MOE_MAX_VOCAB 1048576
+
+/*
+ * moe_token_logprobs -- for rows of logits x, z = scale[t] * x and p = softmax(z):
+ *   logprob[t, j] = log p[ids[t, j]],  entropy[t] = -sum_v p[v] log p[v],
+ *   top_ids[t, i], top_logprob[t, i]: the tokens with the largest logits, equal ones by
+ *   the lower id (-0.0 and +0.0 are equal), and their log p.
+ *   logits   [device] [T, V] of dtype (F32, BF16, F16), rows ld apart, at any alignment
+ *            of their elements.  -inf masks a token: p = 0, log p = -inf, and no list
+ *            names it.  The type's lowest finite value is a logit like any other.
+ *   scale    [device] fp32 [T] (1 / temperature), or NULL: 1.
+ *   ids      [device] int32 or int64 (id_bits 32, 64) [T, m], or NULL (m 0).  An id
+ *            outside [0, V) gets NaN.
+ *   logprob  [device] fp32 [T, m];  entropy [device] fp32 [T] or NULL;
+ *   top_ids  [device] int32 [T, top], top_logprob [device] fp32 [T, top].
+ *   Where fewer than `top` tokens are left, the others are -1 with -inf.  A row that is
+ *   masked as a whole has entropy 0, log p -inf everywhere and no best tokens; a row that
+ *   holds a NaN or +inf, or whose scale is not a positive finite number, NaN in place of
+ *   each log p and entropy, and top_ids -1.
+ *   workspace [device] >= moe_token_logprobs_workspace_bytes(), 256-byte aligned.
+ *   Limits: 1 <= V <= MOE_MAX_VOCAB, 0 <= m <= 1024, 0 <= top <= MOE_MAX_TOP.
+ *   fp32 sums; a row's bits do not depend on T and are the same run to run.
+ */
+typedef struct moe_logprobs {
+    const void* logits;       int64_t ld;
+    const float* scale;
+    const void* ids;
+    float* logprob;
+    float* entropy;
+    int32_t* top_ids;
+    float* top_logprob;
+    int32_t V, m, top, dtype, id_bits, reserved;
+} moe_logprobs;
+
+size_t moe_token_logprobs_workspace_bytes(int64_t T, int32_t V, int32_t top);
+int moe_token_logprobs(const moe_logprobs* args, int64_t T, void* workspace,
+                       size_t workspace_bytes, void* stream);
+
+/* ------------------------------------------- low-rank adapters beside a projection */
+
+#define MOE_MAX_ADAPTERS 1023
+#define MOE_MAX_RANK     256
+
+/*
+ * n slots of low-rank adapters of one projection [N, K], each of its own rank up to
+ * `rank`.  Host struct; a, b, ranks and scales [device], written by moe_pack_adapter:
+ *   a       n * moe_adapter_bytes(0, ..) bytes, b  n * moe_adapter_bytes(1, ..), 16-byte
+ *           aligned
+ *   ranks   int32 [n], 0: an empty slot, which adds nothing (zeros before the first use)
+ *   scales  fp32 [n]
+ */
+typedef struct moe_adapters {
+    int32_t n, rank, K, N;
+    int32_t w_dtype, reserved;          /* MOE_DT_BF16 or MOE_DT_F16 */
+    const void* a;
+    const void* b;
+    const int32_t* ranks;
+    const float* scales;
+} moe_adapters;
+
+/* Bytes of one slot's A (which = 0, [rank, K]) or B (1, [N, rank]); 0 on bad sizes. */
+size_t moe_adapter_bytes(int which, int32_t rank, int32_t K, int32_t N);
+
+/*
+ * moe_pack_adapter -- write a slot: A [rank, K] (rows lda apart) and B [N, rank] (rows ldb
+ * apart), [device], of w_dtype; rank 0 (a, b NULL) empties it.  Ordered on the stream like
+ * any other call: later calls, also of captured graphs, see the new adapter.
+ */
+int moe_pack_adapter(const moe_adapters* set, int32_t slot, const void* a, int64_t lda,
+                     const void* b, int64_t ldb, int32_t rank, float scale, void* stream);
+
+/*
+ * moe_adapter_plan -- a batch's tokens by adapter, for every projection of every layer.
+ *   ids   [device] int32 [T]: each token's slot, outside [0, n): no adapter.
+ *   plan  [device] out, moe_adapter_plan_bytes(T, n) bytes, 16-byte aligned.
+ */
+size_t moe_adapter_plan_bytes(int64_t T, int32_t n);
+int moe_adapter_plan(const int32_t* ids, int64_t T, int32_t n, void* plan, size_t plan_bytes,
+                     void* stream);
+
+/*
+ * moe_add_adapters -- out[t] = y[t] + scales[a] * B_a (A_a x[t]), a the adapter of token t
+ * (none, or an empty slot: out[t] = y[t]); sums in fp32, one rounding to y_dtype.
+ *   x          [device] [T, K] of w_dtype, rows ldx apart, or codes (MOE_DT_I8, rows and
+ *              x_scale as moe_quantize_i8 writes them).
+ *   plan       of the same T and n.
+ *   y, out     [device] [T, N] of y_dtype (F32, BF16, F16), rows ldy and ldo apart; out may
+ *              be y itself (with its stride), else it overlaps no operand.
+ *   workspace  [device] >= moe_add_adapters_workspace_bytes(), 256-byte aligned.
+ *   A x is kept to 2^-16 of itself or better where y_dtype is 16 bits wide, and to 2^-21 of the
+ *   token's largest or better where it is F32.  An infinity or NaN of x touches its own
+ *   token only.  A token's bits depend on its row and its adapter alone.
+ */
+size_t moe_add_adapters_workspace_bytes(const moe_adapters* set, int64_t T);
+int moe_add_adapters(const moe_adapters* set, const void* x, int32_t x_dtype, int64_t ldx,
+                     const float* x_scale, const void* plan, int64_t T, const void* y, int64_t ldy,
+                     void* out, int64_t ldo, int32_t y_dtype, void* workspace,
+                     size_t workspace_bytes, void* stream);
 
 /* ------------------------------------------------------- host-side packers */
 
