@@ -176,8 +176,9 @@ int moe_adapter_plan(const int32_t* ids, int64_t T, int32_t n, void* plan, size_
 }
 
 size_t moe_add_adapters_workspace_bytes(const moe_adapters* set, int64_t T) {
-    if (!set || T < 0 || T >= kMaxRows || set->rank < 1 || set->rank > MOE_MAX_RANK) return 0;
-    return align_up((size_t)T * (size_t)ad_rank_tiles(set->rank) * 64);
+    if (!set || !moe_adapter_plan_bytes(T, set->n) || set->rank < 1 || set->rank > MOE_MAX_RANK || set->K < 1)
+        return 0;
+    return align_up(add_adapters_ws_bytes(*set, T));
 }
 
 int moe_add_adapters(const moe_adapters* set, const void* x, int32_t x_dtype, int64_t ldx,
@@ -209,7 +210,10 @@ int moe_add_adapters(const moe_adapters* set, const void* x, int32_t x_dtype, in
     if (!ws || ws_bytes < need)
         return fail(MOE_EWORKSPACE, fn + ": workspace needs " + std::to_string(need) + " bytes");
     if (!aligned(ws, kAlign)) return bad(fn, "workspace must be 256-byte aligned");
-    if (ad_plan(T, set->n).max_tiles * ad_rank_tiles(set->rank) >= rows_of_launch(16))
+    // the shrink's grid, at most: 16-token pieces by rank tiles by parts
+    const AdPlan lay = ad_plan(T, set->n);
+    if (lay.tiles * (lay.tile / 16) * ad_rank_tiles(set->rank) * kAdParts >=
+        rows_of_launch(kAdWaves))
         return fail(MOE_EUNSUPPORTED, fn + ": too many tokens for one call");
     return launch_add_adapters(*set, x, x_dtype, ldx, x_scale, static_cast<const int32_t*>(plan),
                                T, y, out, y_dtype, ldy, ldo, static_cast<float*>(ws), stream);

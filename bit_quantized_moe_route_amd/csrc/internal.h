@@ -264,32 +264,41 @@ int launch_logprobs(const moe_logprobs& P, int64_t T, void* ws, void* stream);
 // Low-rank adapters.  A's tiles: 16 ranks x 32 inputs, 1 KB in the order of the
 // matrix instruction's operand (lane L: rank L & 15, inputs (L >> 4) * 8 + 0..7), by
 // adapter, rank tile, input tile; the inputs padded with zeros to whole chains.
-// B's: 16 channels x 16 ranks, 512 bytes (lane L of 32: row L & 15, ranks (L >> 4) * 8
-// + 0..7), by adapter, group of 64 channels, rank tile, row tile j of 4; row r of tile
-// j is channel (j >> 1) * 32 + (r >> 2) * 8 + (j & 1) * 4 + (r & 3) of the group, so
-// that a lane's results are 8 neighbouring channels, twice.
+// B's: 64 channels x 16 ranks, 2 KB in two halves (lane L: ranks (L >> 4) * 4 + 0..3 of two
+// channels), by adapter, group of 64 channels, rank tile.  Row r of row tile j of 4 is
+// channel (j >> 1) * 32 + (r >> 2) * 8 + (j & 1) * 4 + (r & 3), so that a lane's results are
+// 8 neighbouring channels, twice; half j >> 1, row L & 15 of tile j in bytes (j & 1) * 8 on.
 constexpr int kAdChain = 128;                  // inputs summed in one go
-constexpr int kAdTile = 16;                    // tokens of a tile
+constexpr int kAdParts = 4, kAdWaves = 4;      // chain c goes to wave c % 16: part, wave of it
 inline int64_t ad_rank_tiles(int32_t rank) { return round_up(rank, 16) / 16; }
+inline int64_t ad_chains(int32_t K) { return round_up(K, kAdChain) / kAdChain; }
+inline int ad_parts(int32_t K) {
+    const int64_t c = (ad_chains(K) + kAdWaves - 1) / kAdWaves;
+    return (int)(c < kAdParts ? c : kAdParts);
+}
 inline int64_t ad_a_bytes(int32_t rank, int32_t K) {
-    return ad_rank_tiles(rank) * (round_up(K, kAdChain) / 32) * 1024;
+    return ad_rank_tiles(rank) * ad_chains(K) * (kAdChain / 32) * 1024;
 }
 inline int64_t ad_b_bytes(int32_t rank, int32_t N) {
     return round_up(N, 64) / 64 * ad_rank_tiles(rank) * 2048;
 }
-// What a plan holds, in int32 from its start: the tokens by adapter (those without
-// one last), tiles of one adapter each (adapter, first, tokens, 0), and the sort's
-// own arrays.  max_tiles bounds the tiles' number, which is at 0.
+// What a plan holds, in int32 from its start: records of tiles of up to `tile` tokens
+// of one adapter (adapter, place of the first in the order, tokens, 0, then the tokens,
+// the last one repeated), no tokens in those past the last; then the sort's own arrays,
+// among them the order: tokens by adapter, those without one last.  Tiles of 64 share
+// their adapter's weights where a slot has 32 tokens or more.
 struct AdPlan {
-    int64_t order, tiles, ids, counts, offsets, inv, ws, total;
-    int64_t max_tiles;
+    int64_t order, ids, counts, offsets, inv, ws, total;
+    int64_t tiles;      // records
+    int tile, rec;      // tokens and int32 of a record
 };
 inline AdPlan ad_plan(int64_t T, int32_t n) {
     AdPlan p;
-    p.max_tiles = T / kAdTile + (T < n + 1 ? T : n + 1);
-    p.order = 4;
-    p.tiles = p.order + round_up(T, 4);
-    p.ids = p.tiles + 4 * p.max_tiles;
+    p.tile = T >= 512 && T >= 32 * (int64_t)n ? 64 : 16;
+    p.rec = 4 + p.tile;
+    p.tiles = T / p.tile + (T < n + 1 ? T : n + 1);
+    p.order = p.tiles * p.rec;
+    p.ids = p.order + round_up(T, 4);
     p.counts = p.ids + round_up(T, 4);
     p.offsets = p.counts + round_up(n + 1, 4);
     p.inv = p.offsets + round_up(n + 2, 4);
@@ -300,6 +309,7 @@ inline AdPlan ad_plan(int64_t T, int32_t n) {
 int launch_adapter_plan(const int32_t* ids, int64_t T, int32_t n, int32_t* plan, void* stream);
 int launch_pack_adapter(const moe_adapters& S, int32_t slot, const void* a, int64_t lda,
                         const void* b, int64_t ldb, int32_t rank, float scale, void* stream);
+size_t add_adapters_ws_bytes(const moe_adapters& S, int64_t T);
 int launch_add_adapters(const moe_adapters& S, const void* x, int32_t x_dtype, int64_t ldx,
                         const float* x_scale, const int32_t* plan, int64_t T, const void* y,
                         void* out, int32_t y_dtype, int64_t ldy, int64_t ldo, float* h,

@@ -259,35 +259,39 @@ __global__ __launch_bounds__(64 * kSmallMaxWaves) void k_route_permute_small(
 
 // ---------------------------------------------------------------- adapter plans
 // The tokens of a batch sorted by the adapter of their request (an id outside [0, n)
-// is none, bin n), and tiles of up to kAdTile tokens of one adapter.
+// is none, bin n), and records of tiles of one adapter.
 __device__ __forceinline__ int adapter_bin(int id, int n) { return id >= 0 && id < n ? id : n; }
 
-// The tile list from each bin's count and first slot (threads tid < E hold bin tid's).
-// base, first, number: LDS [kPermThreads].
+// The tile records from each bin's count and first slot (threads tid < E hold bin
+// tid's); the order is written.  base, firsts, counts: LDS [kPermThreads].
 __device__ __forceinline__ void write_tiles(int count, int first, int E, int* base, int* firsts,
-                                            int* counts, int* wtot, int32_t* plan, int64_t tiles) {
+                                            int* counts, int* wtot, int32_t* plan,
+                                            const AdPlan& L) {
     const int tid = threadIdx.x;
-    const int mine = tid < E ? (count + kAdTile - 1) / kAdTile : 0;
+    const int mine = tid < E ? (count + L.tile - 1) / L.tile : 0;
     const int at = block_exclusive_scan(mine, wtot);
     base[tid] = at;
     firsts[tid] = first;
     counts[tid] = count;
-    if (tid == E - 1) plan[0] = at + mine;
     __syncthreads();
-    const int total = base[E - 1] + (counts[E - 1] + kAdTile - 1) / kAdTile;
-    for (int i = tid; i < total; i += kPermThreads) {
+    const int total = base[E - 1] + (counts[E - 1] + L.tile - 1) / L.tile;
+    for (int64_t x = tid; x < L.tiles * L.tile; x += kPermThreads) {
+        const int i = (int)(x / L.tile), j = (int)(x % L.tile);
+        int32_t* rec = plan + (int64_t)i * L.rec;
+        if (i >= total) {
+            if (j < 4) rec[j] = j == 0 ? E - 1 : 0;
+            continue;
+        }
         int lo = 0, hi = E;                       // base[lo] <= i < base[hi]
         while (hi - lo > 1) {
             const int mid = (lo + hi) / 2;
             if (base[mid] <= i) lo = mid;
             else hi = mid;
         }
-        const int skip = (i - base[lo]) * kAdTile;
-        int32_t* t = plan + tiles + 4 * (int64_t)i;
-        t[0] = lo;
-        t[1] = firsts[lo] + skip;
-        t[2] = min(counts[lo] - skip, kAdTile);
-        t[3] = 0;
+        const int skip = (i - base[lo]) * L.tile;
+        const int n = min(counts[lo] - skip, L.tile);
+        if (j < 4) rec[j] = j == 0 ? lo : j == 1 ? firsts[lo] + skip : j == 2 ? n : 0;
+        rec[4 + j] = plan[L.order + firsts[lo] + skip + min(j, n - 1)];
     }
 }
 
@@ -304,7 +308,7 @@ __global__ __launch_bounds__(kPermThreads) void k_plan(const int32_t* __restrict
     permute_body(sids, T, E, plan + L.counts, plan + L.offsets, plan + L.order, plan + L.inv, smem);
     const int c = tid < E ? smem[tid] : 0;        // the histogram, and the bins' ends
     const int end = tid < E ? smem[E + tid] : 0;
-    write_tiles(c, end - c, E, base, firsts, number, smem + 2 * E, plan, L.tiles);
+    write_tiles(c, end - c, E, base, firsts, number, smem + 2 * E, plan, L);
 }
 
 __global__ __launch_bounds__(256) void k_adapter_bins(const int32_t* __restrict__ ids, int64_t T,
@@ -319,7 +323,7 @@ __global__ __launch_bounds__(kPermThreads) void k_plan_tiles(int n, int32_t* pla
     const int tid = threadIdx.x, E = n + 1;
     const int c = tid < E ? plan[L.counts + tid] : 0;
     const int f = tid < E ? plan[L.offsets + tid] : 0;
-    write_tiles(c, f, E, base, firsts, number, wtot, plan, L.tiles);
+    write_tiles(c, f, E, base, firsts, number, wtot, plan, L);
 }
 
 }  // namespace

@@ -66,7 +66,8 @@ def close(got, x, ids, known, y, w_dtype, what):
 @pytest.mark.parametrize("T,n,rank,K,N", [
     (1, 1, 16, 256, 128), (1, 3, 1, 1, 1), (2, 2, 8, 7, 9), (5, 4, 17, 129, 65), (16, 1, 32, 2048, 64),
     (17, 1, 64, 130, 200), (40, 8, 48, 1001, 250), (64, 64, 16, 512, 1000), (33, 3, 100, 300, 72),
-    (20, 2, 256, 640, 333), (70, 1023, 4, 64, 40), (1030, 5, 40, 333, 130), (1100, 3, 130, 200, 88)])
+    (20, 2, 256, 640, 333), (70, 1023, 4, 64, 40), (1030, 5, 40, 333, 130), (1100, 3, 130, 200, 88), (600, 2, 16, 2100, 70),
+    (640, 20, 32, 100, 300), (513, 16, 64, 3100, 64)])
 def test_products(T, n, rank, K, N, w, x, y):
     say("adapters", T, n, rank, K, N, w, x, y)
     rs = np.random.default_rng(T + K + N)
@@ -91,7 +92,7 @@ def test_products(T, n, rank, K, N, w, x, y):
     assert again is yt and torch.equal(yt, got)
 
 
-@pytest.mark.parametrize("T,n", [(1, 1), (1, 1023), (15, 3), (4096, 7), (4097, 7), (4097, 1023),
+@pytest.mark.parametrize("T,n", [(1, 1), (1, 1023), (15, 3), (511, 3), (512, 16), (512, 17), (4096, 7), (4097, 7), (4097, 1023),
                                  (9000, 1), (20000, 300)])
 def test_plans(T, n):
     """Every token once, by its adapter, in tiles of one adapter."""
@@ -102,19 +103,24 @@ def test_plans(T, n):
     plan = moeq.adapter_plan(torch.from_numpy(ids).to(DEV), n)
     p = plan.data.view(torch.int32).cpu().numpy()
     bins = np.where((ids >= 0) & (ids < n), ids, n)
-    order = p[4:4 + T]
+    tile = 64 if T >= 512 and T >= 32 * n else 16
+    tiles = T // tile + min(T, n + 1)
+    recs = p[:tiles * (4 + tile)].reshape(tiles, 4 + tile)
+    order = p[recs.size:recs.size + T]
     assert np.array_equal(order, np.argsort(bins, kind="stable"))
-    begin = 4 + (T + 3) // 4 * 4
-    tiles = p[begin:begin + 4 * p[0]].reshape(-1, 4)
-    assert p[0] == sum(-(-c // 16) for c in np.bincount(bins))
+    used = sum(-(-c // tile) for c in np.bincount(bins))
     at = 0
-    for a, first, count, zero in tiles.tolist():
-        assert first == at and 1 <= count <= 16 and zero == 0
-        assert np.all(bins[order[first:first + count]] == a)
+    for rec in recs[:used]:
+        a, first, count, zero = rec[:4].tolist()
+        assert first == at and 1 <= count <= tile and zero == 0
+        mine = order[first:first + count]
+        assert np.all(bins[mine] == a) and np.array_equal(rec[4:4 + count], mine)
+        assert np.all(rec[4 + count:] == mine[-1])
         at += count
-    assert at == T
+    assert at == T and np.all(recs[used:, 0] == n) and not recs[used:, 1:4].any()
     again = moeq.adapter_plan(torch.from_numpy(ids).to(DEV), n, plan)
-    assert again is plan and np.array_equal(plan.data.view(torch.int32).cpu().numpy()[:begin], p[:begin])
+    assert again is plan and np.array_equal(plan.data.view(torch.int32).cpu().numpy()[:recs.size + T],
+                                            p[:recs.size + T])
 
 
 def test_many_tokens():
