@@ -62,10 +62,53 @@ __device__ __forceinline__ float elem_of(const Raw8& r, int e) {
     }
 }
 
+// The largest and smallest of three; a NaN is not looked at.  (The compiler's own form
+// of fmaxf first quiets every loaded value, an instruction more each.)
+__device__ __forceinline__ float max3(float a, float b, float c) {
+    float r;
+    asm("v_max3_f32 %0, %1, %2, %3" : "=v"(r) : "v"(a), "v"(b), "v"(c));
+    return r;
+}
+__device__ __forceinline__ float min3(float a, float b, float c) {
+    float r;
+    asm("v_min3_f32 %0, %1, %2, %3" : "=v"(r) : "v"(a), "v"(b), "v"(c));
+    return r;
+}
+
+// Over the wave, the same in every lane: DPP steps inside rows of 16 lanes, then the
+// four rows.
+template <class F>
+__device__ __forceinline__ float wave_all(float v, F f) {
+    auto step = [&](auto ctrl) {
+        const int u = (int)__float_as_uint(v);
+        v = f(v, __uint_as_float((uint32_t)__builtin_amdgcn_update_dpp(
+                     u, u, decltype(ctrl)::value, 0xf, 0xf, false)));
+    };
+    step(std::integral_constant<int, 0xB1>{});
+    step(std::integral_constant<int, 0x4E>{});
+    step(std::integral_constant<int, 0x141>{});
+    step(std::integral_constant<int, 0x140>{});
+    auto lane = [&](int i) {
+        return __uint_as_float(
+            (uint32_t)__builtin_amdgcn_readlane((int)__float_as_uint(v), i));
+    };
+    return f(f(lane(0), lane(16)), f(lane(32), lane(48)));
+}
+__device__ __forceinline__ float all_max(float v) {
+    return wave_all(v, [](float a, float b) { return fmaxf(a, b); });
+}
+__device__ __forceinline__ float all_sum(float v) {
+    return wave_all(v, [](float a, float b) { return a + b; });
+}
+
+// 16-bit logits: 64 registers, so that four workgroups share a CU and some of them load
+// while the others reduce (2048 rows of 131072 bf16, 8 best tokens: 123 us against 133).
 template <int DT, bool TOP>
-__global__ __launch_bounds__(kThreads) void k_slice(LogArgs A) {
+__global__ __launch_bounds__(kThreads, DT == MOE_DT_F32 ? 4 : 8) void k_slice(LogArgs A) {
     constexpr int B = DT == MOE_DT_F32 ? 4 : 2;
-    __shared__ uint32_t order[kThreads];
+    // the low bits of a logit's order that are the same in all of them
+    constexpr int SH = DT == MOE_DT_F32 ? 0 : DT == MOE_DT_BF16 ? 16 : 13;
+    __shared__ uint32_t order[TOP ? kThreads : 1];
     __shared__ float wred[3][kWaves];
     __shared__ uint32_t bound[2];                            // order and place of the bound
     __shared__ int ncol, ncand;
@@ -73,7 +116,8 @@ __global__ __launch_bounds__(kThreads) void k_slice(LogArgs A) {
     __shared__ __attribute__((aligned(16))) uint8_t cols[TOP ? kCols * kChunks * 8 * B : 16];
     __shared__ uint64_t cand[TOP ? kCols * kChunks * 8 : 1];
     const moe_logprobs& P = A.P;
-    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+    const int tid = threadIdx.x, lane = tid & 63;
+    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int64_t t = A.t0 + blockIdx.x / A.S;
     const int slice = blockIdx.x % A.S;
     const int v0 = slice * kSlice;
@@ -81,44 +125,57 @@ __global__ __launch_bounds__(kThreads) void k_slice(LogArgs A) {
 
     // ------------------------------------------------ the slice, and its largest
     Raw8 x[kChunks];
+    if (v0 + kSlice <= P.V) {
 #pragma unroll
-    for (int c = 0; c < kChunks; ++c) {
-        const int v = v0 + (c * kThreads + tid) * 8;
-        if (v + 8 <= P.V) {
-            x[c] = load_raw8<true, true>(row, DT, v);
-        } else {
-            // past the row: -inf
-            const uint32_t none = DT == MOE_DT_F32 ? 0xff800000u
-                                  : DT == MOE_DT_BF16 ? 0xff80ff80u : 0xfc00fc00u;
+        for (int c = 0; c < kChunks; ++c)
+            x[c] = load_raw8<true, true>(row, DT, v0 + (c * kThreads + tid) * 8);
+    } else {
+        // past the row: -inf
+        const uint32_t none = DT == MOE_DT_F32 ? 0xff800000u
+                              : DT == MOE_DT_BF16 ? 0xff80ff80u : 0xfc00fc00u;
+#pragma unroll
+        for (int c = 0; c < kChunks; ++c) {
+            const int v = v0 + (c * kThreads + tid) * 8;
             x[c].a = x[c].b = u32x4{none, none, none, none};
+            if (v + 8 <= P.V) {
+                x[c] = load_raw8<true, true>(row, DT, v);
+            } else if (v < P.V) {
 #pragma unroll
-            for (int e = 0; e < 8; ++e) {
-                if (v + e >= P.V) continue;
-                if constexpr (DT == MOE_DT_F32) {
-                    const uint32_t w = reinterpret_cast<const uint32_t*>(row)[v + e];
-                    if (e < 4) x[c].a[e & 3] = w;
-                    else x[c].b[e & 3] = w;
-                } else {
-                    const uint32_t w = reinterpret_cast<const uint16_t*>(row)[v + e];
-                    const uint32_t o = x[c].a[e >> 1];
-                    x[c].a[e >> 1] = e & 1 ? (o & 0xffffu) | w << 16 : (o & 0xffff0000u) | w;
+                for (int e = 0; e < 8; ++e) {
+                    if (v + e >= P.V) continue;
+                    if constexpr (DT == MOE_DT_F32) {
+                        const uint32_t w = reinterpret_cast<const uint32_t*>(row)[v + e];
+                        if (e < 4) x[c].a[e & 3] = w;
+                        else x[c].b[e & 3] = w;
+                    } else {
+                        const uint32_t w = reinterpret_cast<const uint16_t*>(row)[v + e];
+                        const uint32_t o = x[c].a[e >> 1];
+                        x[c].a[e >> 1] = e & 1 ? (o & 0xffffu) | w << 16 : (o & 0xffff0000u) | w;
+                    }
                 }
             }
         }
     }
-    float best = -__builtin_inff();
+    float best = -__builtin_inff(), least = __builtin_inff();
 #pragma unroll
     for (int c = 0; c < kChunks; ++c)
 #pragma unroll
-        for (int e = 0; e < 8; ++e) best = fmaxf(best, elem_of<DT>(x[c], e));
-    if constexpr (TOP) order[tid] = order_of(best);
-    float m = best;
+        for (int e = 0; e < 8; e += 2) {
+            const float u = elem_of<DT>(x[c], e), v = elem_of<DT>(x[c], e + 1);
+            best = max3(best, u, v);
+            least = min3(least, u, v);
+        }
+    if constexpr (DT != MOE_DT_F32) {
+        // converted again below: 16 registers of 16-bit logits live on, not 32
 #pragma unroll
-    for (int off = 32; off >= 1; off >>= 1) m = fmaxf(m, __shfl_xor(m, off));
-    if (lane == 0) wred[0][wave] = m;
+        for (int c = 0; c < kChunks; ++c) asm volatile("" : "+v"(x[c].a));
+    }
+    if constexpr (TOP) order[tid] = order_of(best);
+    const float wmax = all_max(best);
+    if (lane == 0) wred[0][wave] = wmax;
     if (tid == 0) ncol = ncand = 0;
     __syncthreads();
-    m = wred[0][0];
+    float m = wred[0][0];
 #pragma unroll
     for (int w = 1; w < kWaves; ++w) m = fmaxf(m, wred[0][w]);
     const float mx = m;
@@ -127,61 +184,81 @@ __global__ __launch_bounds__(kThreads) void k_slice(LogArgs A) {
     // ------------------------------------------------ a bound that the n best reach
     if constexpr (TOP) {
         if (wave == 0) {
-            uint32_t o[kWaves];
+            // The largest of 64 groups of threads: the n-th of these is reached by n
+            // logits at least, and by few threads more than n.  A bisection between the
+            // smallest and the largest group; it ends where a quarter too many reach it.
+            uint32_t o[kWaves], top = 0u;
 #pragma unroll
-            for (int i = 0; i < kWaves; ++i) o[i] = order[i * 64 + lane];
+            for (int i = 0; i < kWaves; ++i) {
+                o[i] = order[i * 64 + lane] >> SH;
+                top = max(top, o[i]);
+            }
             auto reach = [&](uint32_t b) {
                 int n = 0;
 #pragma unroll
                 for (int i = 0; i < kWaves; ++i) n += __popcll(__ballot(o[i] >= b));
                 return n;
             };
-            // lo is reached by more than kCols maxima or by all there are, hi by fewer than n
-            uint32_t lo = 1u, place = 0xffffffffu;
-            int n = reach(lo);
+            // lo is reached by n groups at least (or by all there are), hi by fewer
+            uint32_t lo = max(~wave_max_u32(~top), 1u), place = 0xffffffffu;
+            const uint32_t end = (order_of(mx) >> SH) + 1u;
+            uint32_t hi = end;
+            int n = __popcll(__ballot(top >= lo));
+            while (n > P.top + P.top / 4 && hi - lo > 1u) {
+                const uint32_t mid = lo + (hi - lo) / 2;
+                const int k = __popcll(__ballot(top >= mid));
+                if (k < P.top) {
+                    hi = mid;
+                } else {
+                    lo = mid;
+                    n = k;
+                }
+            }
+            n = reach(lo);
             if (n > kCols) {
-                uint32_t hi = mono_bits(mx) + 1u;
+                // Too many threads: the same over all of them.
+                hi = end;
                 while (hi - lo > 1u) {
                     const uint32_t mid = lo + (hi - lo) / 2;
-                    n = reach(mid);
-                    if (n < P.top) {
+                    const int k = reach(mid);
+                    if (k < P.top) {
                         hi = mid;
                     } else {
                         lo = mid;
-                        if (n <= kCols) break;
+                        n = k;
+                        if (k <= kCols) break;
                     }
                 }
-                if (n < P.top || n > kCols) n = reach(lo);
-                if (n > kCols) {
-                    // More threads than kCols whose largest is exactly lo: those with the
-                    // lowest places hold the best of them.  place: the bound of the places.
-                    const int more = P.top - reach(lo + 1u);
-                    uint32_t pl = 0u, ph = (uint32_t)kSlice;        // fewer than more below pl
-                    uint32_t first[kWaves];
+            }
+            if (n > kCols) {
+                // More than kCols threads whose largest is exactly lo: those with the
+                // lowest places hold the best of them.  place: the bound of the places.
+                const int more = P.top - reach(lo + 1u);
+                uint32_t pl = 0u, ph = (uint32_t)kSlice;        // fewer than more below pl
+                uint32_t first[kWaves];
 #pragma unroll
-                    for (int i = 0; i < kWaves; ++i) {
-                        // the lowest place of a thread's logits that equal lo
-                        first[i] = 0xffffffffu;
-                        if (o[i] == lo) {
-                            for (int c = kChunks - 1; c >= 0; --c)
-                                for (int e = 7; e >= 0; --e) {
-                                    const int at = (c * kThreads + i * 64 + lane) * 8 + e;
-                                    if (v0 + at < P.V &&
-                                        order_of(load_elem(row, DT, v0 + at)) == lo)
-                                        first[i] = (uint32_t)at;
-                                }
-                        }
+                for (int i = 0; i < kWaves; ++i) {
+                    // the lowest place of a thread's logits that equal lo
+                    first[i] = 0xffffffffu;
+                    if (o[i] == lo) {
+                        for (int c = kChunks - 1; c >= 0; --c)
+                            for (int e = 7; e >= 0; --e) {
+                                const int at = (c * kThreads + i * 64 + lane) * 8 + e;
+                                if (v0 + at < P.V &&
+                                    order_of(load_elem(row, DT, v0 + at)) >> SH == lo)
+                                    first[i] = (uint32_t)at;
+                            }
                     }
-                    while (ph - pl > 1u) {
-                        const uint32_t mid = pl + (ph - pl) / 2;
-                        int k = 0;
-#pragma unroll
-                        for (int i = 0; i < kWaves; ++i) k += __popcll(__ballot(first[i] < mid));
-                        if (k < more) pl = mid;
-                        else ph = mid;
-                    }
-                    place = ph;          // places are distinct: exactly `more` lie below it
                 }
+                while (ph - pl > 1u) {
+                    const uint32_t mid = pl + (ph - pl) / 2;
+                    int k = 0;
+#pragma unroll
+                    for (int i = 0; i < kWaves; ++i) k += __popcll(__ballot(first[i] < mid));
+                    if (k < more) pl = mid;
+                    else ph = mid;
+                }
+                place = ph;              // places are distinct: exactly `more` lie below it
             }
             if (lane == 0) {
                 bound[0] = lo;
@@ -191,19 +268,31 @@ __global__ __launch_bounds__(kThreads) void k_slice(LogArgs A) {
     }
 
     // ------------------------------------------------ the sums
+    // z = x k - m k in one instruction.  What m k loses in its rounding is the same for
+    // every term of the slice and put back at the end; where m k leaves fp32's range (the
+    // type's lowest value as the largest) it is (x - m) k.
     const float k = scale_of(P, t) * 1.44269504088896340736f;
+    const float mk = m * k, rest = __builtin_fmaf(m, k, -mk);
+    const bool far = !(fabsf(mk) < 0x1p100f), masked = __any(least < -0x1p90f);
     float s = 0.f, d = 0.f;
+    auto sums = [&](auto plain) {
+        constexpr bool PLAIN = decltype(plain)::value;
 #pragma unroll
-    for (int c = 0; c < kChunks; ++c)
+        for (int c = 0; c < kChunks; ++c)
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
-            const float z = (elem_of<DT>(x[c], e) - m) * k;
-            const float p = __builtin_amdgcn_exp2f(z);
-            s += p;
-            d = __builtin_fmaf(p, fmaxf(z, -0x1p100f), d);     // a masked one: 0 * -inf
-        }
-    s = wave_sum(s);
-    d = wave_sum(d);
+            for (int e = 0; e < 8; ++e) {
+                const float v = elem_of<DT>(x[c], e);
+                float z = PLAIN || !far ? __builtin_fmaf(v, k, -mk) : (v - m) * k;
+                const float p = __builtin_amdgcn_exp2f(z);
+                s += p;
+                if constexpr (!PLAIN) z = fmaxf(z, -0x1p100f);     // a masked one: 0 * -inf
+                d = __builtin_fmaf(p, z, d);
+            }
+    };
+    if (far || masked) sums(std::false_type{});
+    else sums(std::true_type{});
+    s = all_sum(s);
+    d = all_sum(d);
     if (lane == 0) {
         wred[1][wave] = s;
         wred[2][wave] = d;
@@ -216,6 +305,12 @@ __global__ __launch_bounds__(kThreads) void k_slice(LogArgs A) {
             ss += wred[1][w];
             dd += wred[2][w];
         }
+        if (!far) {
+            dd = __builtin_fmaf(-rest, ss, dd);
+            const float g = __builtin_amdgcn_exp2f(-rest);
+            ss *= g;
+            dd *= g;
+        }
         A.stat[at] = SliceStat{mx, ss, dd, 0.f};
     }
     if constexpr (!TOP) return;
@@ -223,18 +318,18 @@ __global__ __launch_bounds__(kThreads) void k_slice(LogArgs A) {
     // ------------------------------------------------ the n best
     const uint32_t lo = bound[0], place = bound[1];
     auto reaches = [&](float v, uint32_t p) {
-        const uint32_t o = order_of(v);
+        const uint32_t o = order_of(v) >> SH;
         return o > lo || (o == lo && p < place);
     };
-    if (order_of(best) >= lo) {
-        bool any = place == 0xffffffffu || order_of(best) > lo;
+    const uint32_t mine = order_of(best) >> SH;
+    if (mine >= lo) {
+        bool any = place == 0xffffffffu || mine > lo;
         if (!any) {
-#pragma unroll
             for (int c = 0; c < kChunks; ++c)
-#pragma unroll
-                for (int e = 0; e < 8; ++e)
-                    any = any || reaches(elem_of<DT>(x[c], e),
-                                         (uint32_t)((c * kThreads + tid) * 8 + e));
+                for (int e = 0; e < 8; ++e) {
+                    const int p = (c * kThreads + tid) * 8 + e;
+                    any = any || (v0 + p < P.V && reaches(load_elem(row, DT, v0 + p), (uint32_t)p));
+                }
         }
         if (any) {
             const int j = atomicAdd(&ncol, 1);               // the order changes no result
@@ -251,8 +346,8 @@ __global__ __launch_bounds__(kThreads) void k_slice(LogArgs A) {
     }
     __syncthreads();
     const int nc = min(ncol, kCols) * kChunks;
-    for (int i = tid; i < nc; i += kThreads) {
-        const int place0 = ((i % kChunks) * kThreads + col_of[i / kChunks]) * 8;
+    if (tid < nc) {
+        const int i = tid, place0 = ((i % kChunks) * kThreads + col_of[i / kChunks]) * 8;
         Raw8 r;
         r.a = *reinterpret_cast<const u32x4*>(cols + i * 8 * B);
         if constexpr (DT == MOE_DT_F32) r.b = *reinterpret_cast<const u32x4*>(cols + i * 8 * B + 16);
@@ -274,22 +369,32 @@ __global__ __launch_bounds__(kThreads) void k_slice(LogArgs A) {
     }
     for (int i = n + tid; i < P.top; i += kThreads) out[i] = 0ull;
 }
+static_assert(kCols * kChunks <= kThreads, "a chunk a thread");
 
-// One wave per row: lane s holds slice s.
-__global__ __launch_bounds__(64) void k_join(LogArgs A) {
-    __shared__ uint64_t list[kLogprobSlices * MOE_MAX_TOP];
+// One workgroup per row: a wave, in which lane s holds slice s, or, for the best tokens of
+// few slices, four (FLAT).
+template <bool FLAT>
+__global__ __launch_bounds__(FLAT ? 256 : 64) void k_join(LogArgs A) {
+    __shared__ uint64_t list[FLAT ? 256 : kLogprobSlices * MOE_MAX_TOP];
     const moe_logprobs& P = A.P;
-    const int lane = threadIdx.x;
+    const int tid = threadIdx.x, lane = tid & 63;
     const int64_t t = A.t0 + blockIdx.x;
     const bool in = lane < A.S;
-    const int64_t at = t * A.S + (in ? lane : 0);
     const float NaN = __uint_as_float(0x7fc00000u), inf = __builtin_inff();
-    const SliceStat st = A.stat[at];
-    for (int i = lane; i < A.S * P.top; i += 64) list[i] = A.keys[t * A.S * P.top + i];
+    const SliceStat st = A.stat[t * A.S + (in ? lane : 0)];
+    for (int i = tid; i < A.S * P.top; i += FLAT ? 256 : 64)
+        list[i] = A.keys[t * A.S * P.top + i];
+    auto id_of = [&](int j) {
+        return P.id_bits == 64 ? static_cast<const int64_t*>(P.ids)[t * P.m + j]
+                               : (int64_t) static_cast<const int32_t*>(P.ids)[t * P.m + j];
+    };
+    auto logit_of = [&](int64_t id) {
+        return id >= 0 && id < P.V ? load_elem(P.logits, P.dtype, t * P.ld + id) : NaN;
+    };
+    // the given tokens' logits are on their way before the slices are joined
+    const float given = lane < P.m ? logit_of(id_of(lane)) : 0.f;
     const float sc = scale_of(P, t), k = sc * 1.44269504088896340736f;
-    float M = in ? st.max : -inf;
-#pragma unroll
-    for (int off = 32; off >= 1; off >>= 1) M = fmaxf(M, __shfl_xor(M, off));
+    const float M = all_max(in ? st.max : -inf);
     const bool empty = M == -inf;
     float s = 0.f, d = 0.f;
     if (in) {
@@ -298,46 +403,63 @@ __global__ __launch_bounds__(64) void k_join(LogArgs A) {
         s = st.sum * f;
         d = f * (st.dot + fmaxf(z, -0x1p100f) * st.sum);
     }
-    s = wave_sum(s);
-    d = wave_sum(d);
+    s = all_sum(s);
+    d = all_sum(d);
     const bool bad = !(s >= 0.f);
     const float logS = logf(s);
     auto logprob = [&](float x) {
-        if (bad) return NaN;
+        if (bad || x != x) return NaN;
         return empty || x == -inf ? -inf : (x - M) * sc - logS;
     };
-    if (lane == 0 && P.entropy)
+    if (tid == 0 && P.entropy)
         P.entropy[t] = bad ? NaN : empty ? 0.f : fmaxf(logS - 0.69314718055994530942f * (d / s), 0.f);
-    if (P.ids) {
-        for (int j = lane; j < P.m; j += 64) {
-            const int64_t id = P.id_bits == 64 ? static_cast<const int64_t*>(P.ids)[t * P.m + j]
-                                               : static_cast<const int32_t*>(P.ids)[t * P.m + j];
-            P.logprob[t * P.m + j] =
-                id >= 0 && id < P.V ? logprob(load_elem(P.logits, P.dtype, t * P.ld + id)) : NaN;
-        }
+    if (tid < 64) {
+        if (lane < P.m) P.logprob[t * P.m + lane] = logprob(given);
+        for (int j = lane + 64; j < P.m; j += 64)
+            P.logprob[t * P.m + j] = logprob(logit_of(id_of(j)));
     }
+    if (P.top == 0) return;
     __syncthreads();
-    uint64_t head = P.top && in ? list[lane * P.top] : 0ull;
+    auto put = [&](int place, uint64_t key) {
+        const bool none = bad || key == 0ull;
+        P.top_ids[t * P.top + place] = none ? -1 : (int)(0xffffffffu - (uint32_t)key);
+        P.top_logprob[t * P.top + place] =
+            bad ? NaN : none ? -inf : logprob(mono_float((uint32_t)(key >> 32)));
+    };
+    if constexpr (FLAT) {
+        // A key's place among all of them: how many are larger.
+        const int n = A.S * P.top;
+        const uint64_t key = tid < n ? list[tid] : 0ull;
+        const int all = __syncthreads_count(key != 0ull);
+        if ((tid & ~63) >= n) return;
+        int place = 0;
+#pragma unroll 8
+        for (int j = 0; j < n; ++j) place += list[j] > key;
+        if (key != 0ull && place < P.top) put(place, key);
+        if (tid >= all && tid < P.top) put(tid, 0ull);
+        return;
+    }
+    // The slices' lists are in order: the largest head is the next best token, `top` times.
+    uint64_t head = in ? list[lane * P.top] : 0ull, mine = 0ull;
     int taken = 0;
-    int my_id = -1;
-    float my_lp = bad ? NaN : -inf;
     for (int j = 0; j < P.top; ++j) {
+        const uint64_t next = in && taken + 1 < P.top ? list[lane * P.top + taken + 1] : 0ull;
         const uint32_t hi = (uint32_t)(head >> 32), lo = (uint32_t)head;
         const uint32_t best_hi = wave_max_u32(hi);
         if (best_hi == 0u) break;
-        const uint32_t best_lo = wave_max_u32(hi == best_hi ? lo : 0u);
-        if (lane == j) {
-            my_id = (int)(0xffffffffu - best_lo);
-            my_lp = logprob(mono_float(best_hi));
-        }
+        const uint64_t tied = __ballot(hi == best_hi);
+        uint32_t best_lo;
+        if (__popcll(tied) == 1)
+            best_lo = (uint32_t)__builtin_amdgcn_readlane(lo, __ffsll((unsigned long long)tied) - 1);
+        else
+            best_lo = wave_max_u32(hi == best_hi ? lo : 0u);
+        if (lane == j) mine = (uint64_t)best_hi << 32 | best_lo;
         if (hi == best_hi && lo == best_lo) {
-            head = ++taken < P.top ? list[lane * P.top + taken] : 0ull;
+            head = next;
+            ++taken;
         }
     }
-    if (lane < P.top) {
-        P.top_ids[t * P.top + lane] = bad ? -1 : my_id;
-        P.top_logprob[t * P.top + lane] = my_lp;
-    }
+    if (lane < P.top) put(lane, mine);
 }
 
 }  // namespace
@@ -358,7 +480,10 @@ int launch_logprobs(const moe_logprobs& P, int64_t T, void* ws, void* stream) {
         };
         if (P.top) go(std::true_type{});
         else go(std::false_type{});
-        k_join<<<n, 64, 0, s>>>(A);
+        // Few rows of up to 256 keys: a thread each (32 rows, 20 best of 8 slices: 4.7 us
+        // against 6.6 with one best token after the other; 2048 rows: 8.9 against 5.2).
+        if (P.top && S * P.top <= 256 && T <= 512) k_join<true><<<n, 256, 0, s>>>(A);
+        else k_join<false><<<n, 64, 0, s>>>(A);
     }
     MOEQ_CHECK_LAUNCH();
     return MOE_OK;
