@@ -14,7 +14,8 @@ refuses tensors of several devices.
 import ctypes
 
 from . import _I32, _I64, _P, _torch, lib
-from .block import DT_I8, _call, _cuda, _dt, _flat, _rows, _ws, _x
+from .block import DT_I8, _call, _call_on, _cuda, _dt, _flat, _rows, _x, codes_width
+from .heads import _flat_on, _gpu, _type
 
 MAX_ADAPTERS, MAX_RANK = 1023, 256      # MOE_MAX_ADAPTERS, MOE_MAX_RANK
 
@@ -55,10 +56,11 @@ class Adapters:
         self.b = torch.empty(n * nb, dtype=torch.uint8, device=device)
         self.ranks = torch.zeros(n, dtype=torch.int32, device=device)
         self.scales = torch.zeros(n, dtype=torch.float32, device=device)
-        self.device = self.a.device
+        self.device, self.index, self.w_dtype = self.a.device, self.a.get_device(), _dt(dtype)
         self._c = AdaptersC(n=n, rank=rank, K=K, N=N, w_dtype=_dt(dtype), a=self.a.data_ptr(),
                             b=self.b.data_ptr(), ranks=self.ranks.data_ptr(),
                             scales=self.scales.data_ptr())
+        self.at = ctypes.byref(self._c)
 
     def load(self, slot, a, b, scale=1.0):
         """Puts A [r, K] and B [N, r] (of the set's type) with their scale into a
@@ -89,6 +91,7 @@ class AdapterPlan:
 
     def __init__(self, T, n, data):
         self.T, self.n, self.data, self.device = T, n, data, data.device
+        self.at, self.index = data.data_ptr(), data.get_device()
 
 
 def adapter_plan(ids, n, plan=None):
@@ -111,6 +114,14 @@ def adapter_plan(ids, n, plan=None):
     return plan
 
 
+def _pitch(t, name, T, H):
+    """Elements between the rows of t [T, H], whose own lie side by side."""
+    ld, one = t.stride()
+    if one != 1 and H > 1:
+        raise ValueError(f"the elements of a row of {name} must lie side by side")
+    return ld if T > 1 else max(ld, H)
+
+
 def add_adapters_workspace(adapters, T):
     """Workspace of add_adapters for T tokens."""
     n = lib().moe_add_adapters_workspace_bytes(ctypes.byref(adapters.c()), T)
@@ -122,24 +133,46 @@ def add_adapters(adapters, x, plan, y, scale=None, out=None, ws=None):
     adapters' type, or int8 codes with their scale (quantize_i8, block norms); y
     [T, N] of any float type.  out: of y's type, y itself if not given.  Returns
     out."""
-    dev = _cuda(x, "add_adapters")
-    for t, name in ((adapters, "adapters"), (plan, "plan")):
-        if t.device != dev:
-            raise ValueError(f"x is on {dev}, the {name} on {t.device}")
-    T = x.shape[0]
+    i = _gpu(x, "add_adapters")
+    if adapters.index != i or plan.index != i:
+        raise ValueError(f"x is on {x.device}, the adapters on {adapters.device}, the plan on "
+                         f"{plan.device}")
+    torch = _torch()
+    T, width = x.shape
+    K, N = adapters.K, adapters.N
     if plan.T != T or plan.n != adapters.n:
         raise ValueError(f"the plan is of {plan.T} tokens and {plan.n} adapters, the call of {T} "
                          f"and {adapters.n}")
-    px, dt, ldx, ps = _x(x, scale, adapters.K, dev)
-    if dt != DT_I8 and x.dtype != adapters.dtype:
+    ps = 0
+    if x.dtype is adapters.dtype:
+        dt = adapters.w_dtype
+        if scale is not None:
+            raise ValueError("scales go with int8 codes only")
+        if width != K:
+            raise ValueError(f"x must be [T, {K}], got {list(x.shape)}")
+    elif x.dtype is torch.int8:
+        dt = DT_I8
+        if scale is None:
+            raise ValueError("codes need their scales")
+        if width < codes_width(K):
+            raise ValueError(f"codes must be [T, at least {codes_width(K)}], got {list(x.shape)}")
+        ps = _flat_on(scale, "scale", T, i, torch.float32)
+    else:
         raise ValueError(f"x must be {adapters.dtype} or int8 codes, got {x.dtype}")
-    ldy = _rows(y, "y", T, adapters.N, dev)
+    ldx = _pitch(x, "x", T, width)
     if out is None:
         out = y
-    ldo = _rows(out, "out", T, adapters.N, dev, y.dtype)
-    ws = add_adapters_workspace(adapters, T) if ws is None else _ws(ws, dev)
+    for t, name in ((y, "y"), (out, "out")):
+        if t.shape != (T, N) or t.dtype is not y.dtype or t.get_device() != i:
+            raise ValueError(f"{name} must be [{T}, {N}] of y's type on GPU {i}, got "
+                             f"{list(t.shape)} {t.dtype} on {t.device}")
+    ldy, ldo = _pitch(y, "y", T, N), _pitch(out, "out", T, N)
+    yt = _type(y.dtype)
+    if ws is None:
+        ws = add_adapters_workspace(adapters, T)
+    size = ws.numel()
+    wp = _flat_on(ws, "the workspace", size, i, torch.uint8)
     if T:
-        _call("moe_add_adapters", dev, ctypes.byref(adapters.c()), px, dt, ldx, ps,
-              plan.data.data_ptr(), T, y.data_ptr(), ldy, out.data_ptr(), ldo, _dt(y.dtype),
-              ws.data_ptr(), ws.numel())
+        _call_on("moe_add_adapters", i, adapters.at, x.data_ptr(), dt, ldx, ps, plan.at, T,
+                 y.data_ptr(), ldy, out.data_ptr(), ldo, yt, wp, size)
     return out

@@ -133,22 +133,26 @@ def _bind(L):
     f["lib"] = L
     f["stream"] = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
         lambda i: torch.cuda.current_stream(i).cuda_stream)
-    f["device"] = torch.cuda.current_device
+    f["device"] = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
     _fns = f
     return f
 
 
 def _call(name, dev, *args):
     """One library call on dev and its current stream."""
+    _call_on(name, dev.index, *args)
+
+
+def _call_on(name, i, *args):
+    """One library call on GPU i and its current stream."""
     L = lib()
     f = _fns
     if f.get("lib") is not L:
         f = _bind(L)
-    i = dev.index
     if i == f["device"]():
         st = f[name](*args, f["stream"](i))
     else:
-        with _torch().cuda.device(dev):
+        with _torch().cuda.device(i):
             st = f[name](*args, f["stream"](i))
     if st != MOE_OK:
         _check(st, name)

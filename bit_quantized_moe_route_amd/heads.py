@@ -10,7 +10,7 @@ import ctypes
 import struct
 
 from . import _I32, _I64, _P, _torch, lib
-from .block import _call, _cuda, _dt, _flat, _rows, _ws
+from .block import DT_F32, _call_on, _dt, _dts
 
 MAX_TOP = 32          # MOE_MAX_TOP
 _F32 = ctypes.c_float
@@ -48,14 +48,41 @@ PROTOS = {
 }
 
 
-def _whole(t, name, shape, dev):
-    """Checks whole numbers of `shape` on dev; returns their address and bits."""
-    torch = _torch()
-    if tuple(t.shape) != shape or t.dtype not in (torch.int32, torch.int64) or t.device != dev \
-            or not t.is_contiguous():
-        raise ValueError(f"{name} must be contiguous int32 or int64 {list(shape)} on {dev}, got "
+# The checks go by a tensor's device index: comparing device objects costs twice that, and a
+# call of a few rows is bound by its host side.
+
+_bits = {}
+
+
+def _gpu(t, name):
+    i = t.get_device()
+    if i < 0:
+        raise ValueError(f"{name}: device tensors required")
+    return i
+
+
+def _type(dtype):
+    return _dts.get(dtype) or _dt(dtype)
+
+
+def _flat_on(t, name, n, i, dtype):
+    """Checks a contiguous tensor of n elements of dtype on GPU i."""
+    if t.numel() != n or t.dtype is not dtype or t.get_device() != i or not t.is_contiguous():
+        raise ValueError(f"{name} must be {n} contiguous {dtype} on GPU {i}, got "
                          f"{list(t.shape)} {t.dtype} on {t.device}")
-    return t.data_ptr(), 32 if t.dtype == torch.int32 else 64
+    return t.data_ptr()
+
+
+def _whole(t, name, shape, i):
+    """Checks whole numbers of `shape` on GPU i; returns their address and bits."""
+    if not _bits:
+        torch = _torch()
+        _bits.update({torch.int32: 32, torch.int64: 64})
+    bits = _bits.get(t.dtype)
+    if bits is None or t.shape != shape or t.get_device() != i or not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous int32 or int64 {list(shape)} on GPU {i}, got "
+                         f"{list(t.shape)} {t.dtype} on {t.device}")
+    return t.data_ptr(), bits
 
 
 # --------------------------------------------------------------------------
@@ -80,27 +107,33 @@ def rope_table(positions, rotated, base=10000.0, *, freq=None, scale=1.0, device
     return torch.cat([angle.cos() * scale, angle.sin() * scale], 1).float()
 
 
-def _head_set(x, name, w, out, T, D, dev, dtype, w_dtype):
+def _head_set(x, name, w, out, T, D, i, dtype, w_dtype):
     """The fields of a head set, and its output tensor."""
-    torch = _torch()
-    if x.dim() != 3 or x.shape[0] != T or x.shape[2] != D or x.device != dev or x.dtype != dtype:
-        raise ValueError(f"{name} must be {dtype} [{T}, heads, {D}] on {dev}, got "
-                         f"{list(x.shape)} {x.dtype} on {x.device}")
+    shape = x.shape
+    if len(shape) != 3 or shape[0] != T or shape[2] != D or x.dtype is not dtype \
+            or x.get_device() != i:
+        raise ValueError(f"{name} must be {dtype} [{T}, heads, {D}] on GPU {i}, got "
+                         f"{list(shape)} {x.dtype} on {x.device}")
     if out is None:
-        out = torch.empty(x.shape, dtype=dtype, device=dev)
-    elif out.shape != x.shape or out.device != dev or out.dtype != dtype:
-        raise ValueError(f"{name}_out must be {dtype} {list(x.shape)} on {dev}, got "
+        out = _torch().empty(shape, dtype=dtype, device=x.device)
+    elif out.shape != shape or out.dtype is not dtype or out.get_device() != i:
+        raise ValueError(f"{name}_out must be {dtype} {list(shape)} on GPU {i}, got "
                          f"{list(out.shape)} {out.dtype} on {out.device}")
-    s, o = x.stride(), out.stride()
-    if D > 1 and (s[2] != 1 or o[2] != 1):
+    t, h, e = x.stride()
+    ot, oh, oe = out.stride()
+    if (e != 1 or oe != 1) and D > 1:
         raise ValueError(f"the elements of a head of {name} must lie side by side")
     wp = 0
     if w is not None:
-        if w.shape != (D,) or w.device != dev or w.dtype != w_dtype or not w.is_contiguous():
-            raise ValueError(f"{name}_w must be {w_dtype} [{D}], contiguous, on {dev}, got "
+        if w.shape != (D,) or w.dtype is not w_dtype or w.get_device() != i \
+                or not w.is_contiguous():
+            raise ValueError(f"{name}_w must be {w_dtype} [{D}], contiguous, on GPU {i}, got "
                              f"{list(w.shape)} {w.dtype} on {w.device}")
         wp = w.data_ptr()
-    return (x.data_ptr(), s[0], s[1], out.data_ptr(), o[0], o[1], wp, x.shape[1], 0), out
+    return (x.data_ptr(), t, h, out.data_ptr(), ot, oh, wp, shape[1], 0), out
+
+
+_NO_HEADS = (0, 0, 0, 0, 0, 0, 0, 0, 0)
 
 
 def head_norm_rope(q, k=None, q_w=None, k_w=None, *, pos=None, table=None, interleaved=False,
@@ -113,34 +146,37 @@ def head_norm_rope(q, k=None, q_w=None, k_w=None, *, pos=None, table=None, inter
     b c + a s) with the cosine and sine of table [P, R] (rope_table) at pos [T]
     (none without pos).  q_out and k_out may be q and k.  Returns (q_out, k_out),
     k_out None without k."""
-    torch = _torch()
-    dev = _cuda(q, "head_norm_rope")
-    if q.dim() != 3:
-        raise ValueError(f"q must be [T, heads, D], got {list(q.shape)}")
-    T, _, D = q.shape
-    w_dtype = q_w.dtype if q_w is not None else k_w.dtype if k_w is not None else q.dtype
-    if k is None and (k_w is not None or k_out is not None):
-        raise ValueError("k_w and k_out need k")
-    fq, q_out = _head_set(q, "q", q_w, q_out, T, D, dev, q.dtype, w_dtype)
-    fk = (0, 0, 0, 0, 0, 0, 0, 0, 0)
+    i = _gpu(q, "head_norm_rope")
+    shape = q.shape
+    if len(shape) != 3:
+        raise ValueError(f"q must be [T, heads, D], got {list(shape)}")
+    T, _, D = shape
+    dtype = q.dtype
+    w_dtype = q_w.dtype if q_w is not None else k_w.dtype if k_w is not None else dtype
+    fq, q_out = _head_set(q, "q", q_w, q_out, T, D, i, dtype, w_dtype)
     if k is not None:
-        fk, k_out = _head_set(k, "k", k_w, k_out, T, D, dev, q.dtype, w_dtype)
+        fk, k_out = _head_set(k, "k", k_w, k_out, T, D, i, dtype, w_dtype)
+    elif k_w is not None or k_out is not None:
+        raise ValueError("k_w and k_out need k")
+    else:
+        fk = _NO_HEADS
     pp = tp = bits = rows = R = 0
     if pos is not None:
         if table is None:
             raise ValueError("pos needs a table (rope_table)")
-        if table.dim() != 2 or table.dtype != torch.float32 or table.device != dev \
+        size = table.shape
+        if len(size) != 2 or _type(table.dtype) != DT_F32 or table.get_device() != i \
                 or not table.is_contiguous():
-            raise ValueError(f"table must be contiguous fp32 [positions, R] on {dev}")
-        pp, bits = _whole(pos, "pos", (T,), dev)
-        rows, R = table.shape
+            raise ValueError(f"table must be contiguous fp32 [positions, R] on GPU {i}")
+        pp, bits = _whole(pos, "pos", (T,), i)
+        rows, R = size
         tp = table.data_ptr()
     elif table is not None:
         raise ValueError("table needs pos")
     if T:
-        _call("moe_head_norm_rope", dev,
-              _HEADS.pack(*fq, *fk, pp, tp, rows, D, R, 1 if interleaved else 0, bits, _dt(q.dtype),
-                          _dt(w_dtype), eps, w_offset), T)
+        _call_on("moe_head_norm_rope", i,
+                 _HEADS.pack(*fq, *fk, pp, tp, rows, D, R, 1 if interleaved else 0, bits,
+                             _type(dtype), _type(w_dtype), eps, w_offset), T)
     return q_out, k_out
 
 
@@ -168,44 +204,54 @@ def token_logprobs(logits, ids=None, *, top=0, scale=None, logprob=None, entropy
     A logit of -inf masks its token; a list that runs out of tokens goes on with -1
     and -inf.  A row that is masked as a whole: entropy 0, -inf everywhere.  A row
     with a NaN or +inf, or a scale that is not positive and finite: NaN and -1."""
-    torch = _torch()
-    dev = _cuda(logits, "token_logprobs")
-    if logits.dim() != 2:
-        raise ValueError(f"logits must be [T, V], got {list(logits.shape)}")
-    T, V = logits.shape
-    ld = _rows(logits, "logits", T, V, dev)
+    i = _gpu(logits, "token_logprobs")
+    size = logits.shape
+    if len(size) != 2:
+        raise ValueError(f"logits must be [T, V], got {list(size)}")
+    T, V = size
+    ld, one = logits.stride()
+    if one != 1 and V > 1:
+        raise ValueError("the elements of a row of logits must lie side by side")
+    if T == 1 and ld < V:
+        ld = V
     if not 0 <= top <= MAX_TOP:
         raise ValueError(f"top must be in [0, {MAX_TOP}], got {top}")
+    torch = _torch()
+    f32 = torch.float32
     ip = bits = m = lp = sp = tp = tl = 0
     if ids is not None:
-        if ids.dim() not in (1, 2):
-            raise ValueError(f"ids must be [T] or [T, m], got {list(ids.shape)}")
-        m = 1 if ids.dim() == 1 else ids.shape[1]
-        ip, bits = _whole(ids, "ids", (T,) if ids.dim() == 1 else (T, m), dev)
+        at = ids.shape
+        if len(at) not in (1, 2):
+            raise ValueError(f"ids must be [T] or [T, m], got {list(at)}")
+        m = 1 if len(at) == 1 else at[1]
+        ip, bits = _whole(ids, "ids", (T,) if len(at) == 1 else (T, m), i)
         if logprob is None:
-            logprob = torch.empty(ids.shape, dtype=torch.float32, device=dev)
-        lp = _flat(logprob, "logprob", T * m, dev, torch.float32)
+            logprob = torch.empty(at, dtype=f32, device=logits.device)
+        lp = _flat_on(logprob, "logprob", T * m, i, f32)
     elif logprob is not None:
         raise ValueError("logprob needs ids")
     if scale is not None:
-        sp = _flat(scale, "scale", T, dev, torch.float32)
+        sp = _flat_on(scale, "scale", T, i, f32)
     if entropy is None:
-        entropy = torch.empty(T, dtype=torch.float32, device=dev)
-    ep = _flat(entropy, "entropy", T, dev, torch.float32)
+        entropy = torch.empty(T, dtype=f32, device=logits.device)
+    ep = _flat_on(entropy, "entropy", T, i, f32)
     if top:
         if top_ids is None:
-            top_ids = torch.empty((T, top), dtype=torch.int32, device=dev)
+            top_ids = torch.empty((T, top), dtype=torch.int32, device=logits.device)
         if top_logprob is None:
-            top_logprob = torch.empty((T, top), dtype=torch.float32, device=dev)
-        tp = _flat(top_ids, "top_ids", T * top, dev, torch.int32)
-        tl = _flat(top_logprob, "top_logprob", T * top, dev, torch.float32)
+            top_logprob = torch.empty((T, top), dtype=f32, device=logits.device)
+        tp = _flat_on(top_ids, "top_ids", T * top, i, torch.int32)
+        tl = _flat_on(top_logprob, "top_logprob", T * top, i, f32)
     elif top_ids is not None or top_logprob is not None:
         raise ValueError("top_ids and top_logprob go with top > 0")
-    ws = token_logprobs_workspace(logits, top) if ws is None else _ws(ws, dev)
+    if ws is None:
+        ws = token_logprobs_workspace(logits, top)
+    n = ws.numel()
+    wp = _flat_on(ws, "the workspace", n, i, torch.uint8)
     if T:
         if m == 0:
             ip = lp = 0
-        _call("moe_token_logprobs", dev,
-              _LOGPROBS.pack(logits.data_ptr(), ld, sp, ip, lp, ep, tp, tl, V, m, top,
-                             _dt(logits.dtype), bits, 0), T, ws.data_ptr(), ws.numel())
+        _call_on("moe_token_logprobs", i,
+                 _LOGPROBS.pack(logits.data_ptr(), ld, sp, ip, lp, ep, tp, tl, V, m, top,
+                                _type(logits.dtype), bits, 0), T, wp, n)
     return (logprob, entropy, top_ids, top_logprob) if top else (logprob, entropy)

@@ -294,7 +294,8 @@ def test_binding_refuses_host_tensors():
 
 def test_head_set_checks():
     x = torch.zeros((2, 3, 8))
-    ok, out = mh._head_set(x[:, 1:], "q", None, None, 2, 8, x.device, x.dtype, x.dtype)
+    check = lambda x, w, o: mh._head_set(x, "q", w, o, 2, 8, -1, torch.float32, torch.float32)  # noqa: E731
+    ok, out = check(x[:, 1:], None, None)
     assert ok[1:3] == (24, 8) and out.shape == (2, 2, 8)
     for bad, w, o, says in ((x[0], None, None, "must be"), (x.transpose(1, 2), None, None, "must be"),
                             (torch.zeros(2, 8, 3).transpose(1, 2), None, None, "side by side"),
@@ -302,7 +303,10 @@ def test_head_set_checks():
                             (x, None, torch.zeros(2, 3, 9), "q_out"),
                             (x, None, torch.zeros(2, 3, 8).half(), "q_out")):
         with pytest.raises(ValueError, match=says):
-            mh._head_set(bad, "q", w, o, 2, 8, x.device, x.dtype, x.dtype)
+            check(bad, w, o)
     with pytest.raises(ValueError, match="pos"):
-        mh._whole(torch.zeros(3), "pos", (3,), x.device)
-    assert mh._whole(torch.zeros(3, dtype=torch.int64), "pos", (3,), x.device)[1] == 64
+        mh._whole(torch.zeros(3), "pos", (3,), -1)
+    assert mh._whole(torch.zeros(3, dtype=torch.int64), "pos", (3,), -1)[1] == 64
+    assert ma._pitch(x[0][:, 2:6], "y", 3, 4) == 8 and ma._pitch(x[0][:1, :4], "y", 1, 4) == 8
+    with pytest.raises(ValueError, match="side by side"):
+        ma._pitch(x[0].t(), "y", 8, 3)
