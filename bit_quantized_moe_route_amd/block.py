@@ -379,15 +379,26 @@ def linear_i8_workspace(linear, T):
     return _torch().empty(max(n, 256), dtype=_torch().uint8, device=linear.device)
 
 
-def linear_i8(linear, x, scale=None, out=None, out_dtype=None, ws=None):
+def linear_i8(linear, x, scale=None, out=None, out_dtype=None, ws=None, adapters=None, plan=None,
+              adapter_ws=None):
     """x [T, K] times the matrix, in 8 bits: [T, N] of out_dtype (x's type, bf16
     for codes, by default).  x: float rows, coded in the call, or int8 codes
-    from quantize_i8 or a block norm with their scale."""
+    from quantize_i8 or a block norm with their scale.  With adapters (Adapters of
+    the same K and N) and the batch's plan, add_adapters follows on the result,
+    which is rounded to its type before and after."""
     torch = _torch()
     dev = _cuda(x, "linear_i8")
     if dev != linear.device:
         raise ValueError(f"x is on {dev}, the matrix on {linear.device}")
     T = x.shape[0]
+    if adapters is not None:
+        if (adapters.K, adapters.N) != (linear.K, linear.N) or plan is None or plan.T != T \
+                or plan.n != adapters.n or adapters.device != dev or plan.device != dev \
+                or x.dtype not in (adapters.dtype, torch.int8):
+            raise ValueError("adapters must be of the matrix's K and N and x's device and type, "
+                             "with the batch's plan")
+    elif plan is not None or adapter_ws is not None:
+        raise ValueError("plan and adapter_ws go with adapters")
     px, dt, ldx, ps = _x(x, scale, linear.K, dev)
     if out is None:
         out = torch.empty((T, linear.N), device=dev, dtype=out_dtype or (
@@ -398,6 +409,10 @@ def linear_i8(linear, x, scale=None, out=None, out_dtype=None, ws=None):
     if T:
         _call("moe_linear_i8", dev, ctypes.byref(linear.c()), px, dt, ldx, ps, T, out.data_ptr(),
               _dt(out.dtype), ldo, _dptr(ws), ws.numel() if ws is not None else 0)
+    if adapters is not None:
+        from .adapters import add_adapters
+
+        add_adapters(adapters, x, plan, out, scale=scale, ws=adapter_ws)
     return out
 
 

@@ -103,7 +103,8 @@ __device__ __forceinline__ float all_sum(float v) {
 
 // 16-bit logits: 64 registers, so that four workgroups share a CU and some of them load
 // while the others reduce (2048 rows of 131072 bf16, 8 best tokens: 123 us against 133).
-template <int DT, bool TOP>
+// STREAM: logits that no cache holds.
+template <int DT, bool TOP, bool STREAM>
 __global__ __launch_bounds__(kThreads, DT == MOE_DT_F32 ? 4 : 8) void k_slice(LogArgs A) {
     constexpr int B = DT == MOE_DT_F32 ? 4 : 2;
     // the low bits of a logit's order that are the same in all of them
@@ -128,7 +129,7 @@ __global__ __launch_bounds__(kThreads, DT == MOE_DT_F32 ? 4 : 8) void k_slice(Lo
     if (v0 + kSlice <= P.V) {
 #pragma unroll
         for (int c = 0; c < kChunks; ++c)
-            x[c] = load_raw8<true, true>(row, DT, v0 + (c * kThreads + tid) * 8);
+            x[c] = load_raw8<STREAM, true>(row, DT, v0 + (c * kThreads + tid) * 8);
     } else {
         // past the row: -inf
         const uint32_t none = DT == MOE_DT_F32 ? 0xff800000u
@@ -138,7 +139,7 @@ __global__ __launch_bounds__(kThreads, DT == MOE_DT_F32 ? 4 : 8) void k_slice(Lo
             const int v = v0 + (c * kThreads + tid) * 8;
             x[c].a = x[c].b = u32x4{none, none, none, none};
             if (v + 8 <= P.V) {
-                x[c] = load_raw8<true, true>(row, DT, v);
+                x[c] = load_raw8<STREAM, true>(row, DT, v);
             } else if (v < P.V) {
 #pragma unroll
                 for (int e = 0; e < 8; ++e) {
@@ -472,14 +473,25 @@ int launch_logprobs(const moe_logprobs& P, int64_t T, void* ws, void* stream) {
     const int64_t most = rows_of_launch(kWaves) / S;
     for (A.t0 = 0; A.t0 < T; A.t0 += most) {
         const unsigned n = (unsigned)(T - A.t0 < most ? T - A.t0 : most);
-        auto go = [&](auto top) {
-            constexpr bool TOP = decltype(top)::value;
-            if (P.dtype == MOE_DT_F32) k_slice<MOE_DT_F32, TOP><<<n * S, kThreads, 0, s>>>(A);
-            else if (P.dtype == MOE_DT_BF16) k_slice<MOE_DT_BF16, TOP><<<n * S, kThreads, 0, s>>>(A);
-            else k_slice<MOE_DT_F16, TOP><<<n * S, kThreads, 0, s>>>(A);
+        auto go = [&](auto top, auto stream) {
+            constexpr bool TOP = decltype(top)::value, STREAM = decltype(stream)::value;
+            if (P.dtype == MOE_DT_F32)
+                k_slice<MOE_DT_F32, TOP, STREAM><<<n * S, kThreads, 0, s>>>(A);
+            else if (P.dtype == MOE_DT_BF16)
+                k_slice<MOE_DT_BF16, TOP, STREAM><<<n * S, kThreads, 0, s>>>(A);
+            else
+                k_slice<MOE_DT_F16, TOP, STREAM><<<n * S, kThreads, 0, s>>>(A);
         };
-        if (P.top) go(std::true_type{});
-        else go(std::false_type{});
+        // More logits than the caches hold are read past them (2048 rows of 131072 bf16, no
+        // best tokens: 95.9 us against 102.4); fewer may be found there (32 rows of fp32, 20
+        // best tokens: 13.5 us against 14.4).
+        const bool large = T * P.V * (P.dtype == MOE_DT_F32 ? 4 : 2) >= (int64_t)1 << 28;
+        auto by = [&](auto top) {
+            if (large) go(top, std::true_type{});
+            else go(top, std::false_type{});
+        };
+        if (P.top) by(std::true_type{});
+        else by(std::false_type{});
         // Few rows of up to 256 keys: a thread each (32 rows, 20 best of 8 slices: 4.7 us
         // against 6.6 with one best token after the other; 2048 rows: 8.9 against 5.2).
         if (P.top && S * P.top <= 256 && T <= 512) k_join<true><<<n, 256, 0, s>>>(A);

@@ -298,3 +298,27 @@ def test_stream_and_graph():
         torch.cuda.synchronize()
         want = moeq.add_adapters(s, x, moeq.adapter_plan(ids, n), y, out=torch.empty_like(y))
         assert torch.equal(out, want), i
+
+
+@pytest.mark.parametrize("T,K,N", [(1, 256, 128), (40, 200, 100), (700, 264, 192)])
+def test_beside_an_8_bit_product(T, K, N):
+    """linear_i8 with adapters is the product and then add_adapters, for rows and codes."""
+    rs = np.random.default_rng(17)
+    lin = moeq.I8Linear.quantized(rnd(rs, (N, K), torch.float32))
+    s, _ = make(rs, 3, 16, K, N, torch.bfloat16)
+    ids = rs.integers(-1, 3, T).astype(np.int32)
+    plan = moeq.adapter_plan(torch.from_numpy(ids).to(DEV), 3)
+    x = rnd(rs, (T, K), torch.bfloat16)
+    q, scale = moeq.quantize_i8(x)
+    for rows, sc in ((x, None), (q, scale)):
+        y = moeq.linear_i8(lin, rows, sc, out_dtype=torch.float32)
+        want = moeq.add_adapters(s, rows, plan, y.clone(), scale=sc)
+        got = moeq.linear_i8(lin, rows, sc, out_dtype=torch.float32, adapters=s, plan=plan)
+        assert torch.equal(got, want) and torch.equal(got, y) == (ids < 0).all()
+    other = moeq.Adapters(3, 16, K, N + 1)
+    for kw in (dict(adapters=s), dict(plan=plan), dict(adapters=other, plan=plan),
+               dict(adapters=s, plan=moeq.adapter_plan(torch.zeros(T, dtype=torch.int32, device=DEV), 2))):
+        with pytest.raises(ValueError, match="adapters"):
+            moeq.linear_i8(lin, x, **kw)
+    with pytest.raises(ValueError, match="adapters"):
+        moeq.linear_i8(lin, x.half(), adapters=s, plan=plan)
