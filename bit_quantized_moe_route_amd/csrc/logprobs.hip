@@ -269,12 +269,12 @@ __global__ __launch_bounds__(kThreads, DT == MOE_DT_F32 ? 4 : 8) void k_slice(Lo
     }
 
     // ------------------------------------------------ the sums
-    // z = x k - m k in one instruction.  What m k loses in its rounding is the same for
-    // every term of the slice and put back at the end; where m k leaves fp32's range (the
-    // type's lowest value as the largest) it is (x - m) k.
+    // z = x k - m k in one instruction.  What m k loses in its rounding (under 2^-4) is the
+    // same for every term of the slice and put back at the end; past 2^20 it could be more
+    // than an exponent holds, and z is (x - m) k.
     const float k = scale_of(P, t) * 1.44269504088896340736f;
     const float mk = m * k, rest = __builtin_fmaf(m, k, -mk);
-    const bool far = !(fabsf(mk) < 0x1p100f), masked = __any(least < -0x1p90f);
+    const bool far = !(fabsf(mk) < 0x1p20f), masked = __any(least < -0x1p90f);
     float s = 0.f, d = 0.f;
     auto sums = [&](auto plain) {
         constexpr bool PLAIN = decltype(plain)::value;

@@ -136,6 +136,23 @@ def test_rows_without_a_distribution(dt):
         assert all(torch.equal(a[t], b[t]) for a, b in zip(got, ref))
 
 
+@pytest.mark.parametrize("dt", sorted(TYPES))
+def test_large_magnitudes(dt):
+    """Logits far from zero on either side, up to the type's largest: only differences count."""
+    rs = np.random.default_rng(11)
+    big = float(torch.finfo(TYPES[dt]).max)
+    x = torch.empty((12, 20000), dtype=TYPES[dt], device=DEV)
+    for t, base in enumerate((1e4, 6e5, 9e5, 3e6, 1e10, 1e20, 1e28, 1e30, 1e38)):
+        base = min(base, big / 2)
+        step = base * torch.finfo(TYPES[dt]).eps
+        x[t] = (1 if t % 2 else -1) * base + torch.from_numpy(rs.integers(0, 9, 20000) * step).to(DEV)
+    x[9], x[10], x[11] = big, -big, 0.0
+    x[11, 7], x[11, 9] = -big, big
+    ids = torch.tensor([3, 9], dtype=torch.int32, device=DEV).repeat(12, 1)
+    check(x, 9, ids)
+    check(x, 9, ids, torch.full((12,), 1e-4, device=DEV))
+
+
 def test_ids_outside():
     x = rows(np.random.default_rng(1), 2, 100, torch.float32)
     ids = torch.tensor([[-1, 100, 5], [99, -2 ** 31, 2 ** 31 - 1]], dtype=torch.int32, device=DEV)
