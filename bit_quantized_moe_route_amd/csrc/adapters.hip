@@ -630,19 +630,28 @@ __global__ __launch_bounds__(256) void k_pack(moe_adapters S, int slot, const ui
     }
 }
 
-// The kernels for many tokens: tiles of 64, ranks up to 128.
+// The kernels for many tokens read x and the weights once for all of an adapter's ranks
+// and 32 tokens, the others once for each 16; but fewer workgroups hold less in flight.
+// Ranks 17 to 128 from T times rank tiles 8192 on (6144 -> 6144, 8 adapters, us against
+// the others: rank 64 at 1500 / 2048 / 4096 tokens 34.1 : 32.6, 48.2 : 44.1, 63.9 : 89.9;
+// rank 32 at 2048 / 4096 38.8 : 29.3, 55.3 : 63.3; rank 128 at 1024 / 2048 40.0 : 40.7,
+// 54.1 : 72.9; rank 16 at 4096 51.6 : 47.4).
 bool ad_wide(const moe_adapters& S, int64_t T) {
-    return ad_plan(T, S.n).tile == 64 && ad_rank_tiles(S.rank) <= kWideTiles;
+    const int64_t rt = ad_rank_tiles(S.rank);
+    return ad_plan(T, S.n).tile == 64 && rt >= 2 && rt <= kWideTiles && T * rt >= 8192;
 }
 
 }  // namespace
 
-// h: fp32 parts, or (many tokens) 24 bytes for four ranks of a token and 4 a token.
+// h: fp32 parts, or (many tokens) 24 bytes for four ranks of a token and 4 a token; the
+// larger, so that a workspace serves fewer tokens too.
 size_t add_adapters_ws_bytes(const moe_adapters& S, int64_t T) {
     const AdPlan lay = ad_plan(T, S.n);
     const size_t rt = (size_t)ad_rank_tiles(S.rank);
     const size_t pieces = (size_t)(lay.tiles * (lay.tile / 16));
-    return ad_wide(S, T) ? pieces * (rt * 64 * 24 + 64) : (size_t)T * rt * 64 * ad_parts(S.K);
+    const size_t few = (size_t)T * rt * 64 * ad_parts(S.K);
+    const size_t many = ad_wide(S, T) ? pieces * (rt * 64 * 24 + 64) : 0;
+    return few > many ? few : many;
 }
 
 int launch_pack_adapter(const moe_adapters& S, int32_t slot, const void* a, int64_t lda,
@@ -711,8 +720,6 @@ int launch_add_adapters(const moe_adapters& S, const void* x, int32_t x_dtype, i
             A.pieces = lay.tiles * A.sub;
             A.items = A.pieces * A.rt * A.parts;
             k_shrink<BF, I8><<<(unsigned)A.items, 64 * kAdWaves, 0, s>>>(A);
-        } else if (A.rt == 1) {
-            go(c2, c1);
         } else if (A.rt == 2) {
             go(c2, c2);
         } else if (A.rt <= 4) {
@@ -736,7 +743,7 @@ int launch_add_adapters(const moe_adapters& S, const void* x, int32_t x_dtype, i
             const int64_t n = A.items - A.items0 < max_items ? A.items - A.items0 : max_items;
             auto go = [&](auto yt) {
                 constexpr int YT = decltype(yt)::value;
-                if constexpr (RS <= kWideTiles) {
+                if constexpr (RS > 1 && RS <= kWideTiles) {
                     if (wide) {
                         k_apply<BF, YT, M, RS><<<(unsigned)n, 64 * kAdWaves, 0, s>>>(A);
                         return;

@@ -157,7 +157,9 @@ int moe_pack_adapter(const moe_adapters* set, int32_t slot, const void* a, int64
 
 size_t moe_adapter_plan_bytes(int64_t T, int32_t n) {
     if (T < 0 || T >= kMaxRows - 4096 || n < 1 || n > MOE_MAX_ADAPTERS) return 0;
-    return (size_t)ad_plan(T, n).total * 4;
+    // never less for more tokens: records of 16 would need more than some of 64 do
+    const int64_t some = ad_plan(T, n, 16).total, own = ad_plan(T, n).total;
+    return (size_t)(some > own ? some : own) * 4;
 }
 
 int moe_adapter_plan(const int32_t* ids, int64_t T, int32_t n, void* plan, size_t plan_bytes,

@@ -285,16 +285,16 @@ inline int64_t ad_b_bytes(int32_t rank, int32_t N) {
 // What a plan holds, in int32 from its start: records of tiles of up to `tile` tokens
 // of one adapter (adapter, place of the first in the order, tokens, 0, then the tokens,
 // the last one repeated), no tokens in those past the last; then the sort's own arrays,
-// among them the order: tokens by adapter, those without one last.  Tiles of 64 share
-// their adapter's weights where a slot has 32 tokens or more.
+// among them the order: tokens by adapter, those without one last.  Tiles of 64, which the
+// kernels for many tokens take whole, where a slot has 32 tokens or more.
 struct AdPlan {
     int64_t order, ids, counts, offsets, inv, ws, total;
     int64_t tiles;      // records
     int tile, rec;      // tokens and int32 of a record
 };
-inline AdPlan ad_plan(int64_t T, int32_t n) {
+inline AdPlan ad_plan(int64_t T, int32_t n, int tile) {
     AdPlan p;
-    p.tile = T >= 512 && T >= 32 * (int64_t)n ? 64 : 16;
+    p.tile = tile;
     p.rec = 4 + p.tile;
     p.tiles = T / p.tile + (T < n + 1 ? T : n + 1);
     p.order = p.tiles * p.rec;
@@ -305,6 +305,9 @@ inline AdPlan ad_plan(int64_t T, int32_t n) {
     p.ws = p.inv + round_up(T, 4);
     p.total = p.ws + (int64_t)permute_ws_bytes(T, 1, n + 1) / 4;
     return p;
+}
+inline AdPlan ad_plan(int64_t T, int32_t n) {
+    return ad_plan(T, n, T >= 1024 && T >= 32 * (int64_t)n ? 64 : 16);
 }
 int launch_adapter_plan(const int32_t* ids, int64_t T, int32_t n, int32_t* plan, void* stream);
 int launch_pack_adapter(const moe_adapters& S, int32_t slot, const void* a, int64_t lda,

@@ -781,6 +781,7 @@ int moe_head_norm_rope(const moe_heads* heads, int64_t T, void* stream);
  *   holds a NaN or +inf, or whose scale is not a positive finite number, NaN in place of
  *   each log p and entropy, and top_ids -1.
  *   workspace [device] >= moe_token_logprobs_workspace_bytes(), 256-byte aligned.
+ *   Outputs and workspace overlap no operand and not each other.
  *   Limits: 1 <= V <= MOE_MAX_VOCAB, 0 <= m <= 1024, 0 <= top <= MOE_MAX_TOP.
  *   fp32 sums; a row's bits do not depend on T and are the same run to run.
  */
@@ -836,6 +837,8 @@ int moe_pack_adapter(const moe_adapters* set, int32_t slot, const void* a, int64
  * moe_adapter_plan -- a batch's tokens by adapter, for every projection of every layer.
  *   ids   [device] int32 [T]: each token's slot, outside [0, n): no adapter.
  *   plan  [device] out, moe_adapter_plan_bytes(T, n) bytes, 16-byte aligned.
+ * (These bytes, and those of the workspace below, are never fewer for more tokens: what
+ * serves T tokens serves fewer.)
  */
 size_t moe_adapter_plan_bytes(int64_t T, int32_t n);
 int moe_adapter_plan(const int32_t* ids, int64_t T, int32_t n, void* plan, size_t plan_bytes,

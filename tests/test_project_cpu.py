@@ -253,6 +253,18 @@ def test_add_adapters_refusals(args, status, says):
     refused("moe_add_adapters", adapters(), *args, None, status=status, says=says)
 
 
+@pytest.mark.parametrize("n", [1, 8, 33, 1023])
+@pytest.mark.parametrize("rank,K", [(16, 100), (32, 4096), (64, 6144), (256, 512)])
+def test_bytes_never_fall_with_the_tokens(n, rank, K):
+    s = ma.AdaptersC(n=n, rank=rank, K=K, N=64)
+    Ts = list(range(1, 1100)) + list(range(1100, 9000, 61)) + [n * 32 - 1, n * 32, 40000]
+    Ts.sort()
+    L = moeq.lib()
+    plans = [L.moe_adapter_plan_bytes(T, n) for T in Ts]
+    spaces = [L.moe_add_adapters_workspace_bytes(ctypes.byref(s), T) for T in Ts]
+    assert plans == sorted(plans) and spaces == sorted(spaces)
+
+
 def test_plan_refusals():
     for T, n in ((-1, 1), (1, 0), (1, 1024), (1 << 31, 1)):
         refused("moe_adapter_plan", P, T, n, P, 1 << 20, None)
