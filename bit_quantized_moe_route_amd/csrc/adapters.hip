@@ -16,6 +16,11 @@
 // it enters the second product as the sum of two numbers of the weights' type.  fp16 holds
 // 22 bits of h so, its row first brought to [1, 2) by a power of two; bf16 16 bits, enough
 // for a 16-bit result, and a third number follows where y is fp32.
+//
+// Few tokens are bound by latency: one token, 6144 -> 6144, rank 16: 3.3 and 3.8 us for the
+// two; 64 tokens and as many slots of ranks to 64, 6144 -> 2048: 7.6 and 4.7.  4096 tokens,
+// 8 slots, 6144 -> 6144: 31.5 for the first (1.6 TB/s of x; every 32 tokens read their A
+// from an L2) and 32.5 for the second (3.2 TB/s; a copy in its structure takes 26).
 #include <type_traits>
 
 #include "elem_dev.h"
