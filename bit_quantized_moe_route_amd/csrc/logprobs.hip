@@ -19,7 +19,7 @@
 // HBM bounds large batches: 2048 rows of 131072 in bf16 take 86 us without best tokens
 // (6.2 TB/s), 110 with 8 of them, since a workgroup searches when its loads are done.  A
 // row alone is two launches (5.7 and 3.1 us of kernels), 32 rows of fp32 a single wave of
-// workgroups (9 and 4.8).
+// workgroups (8.7 and 4.8).
 #include "elem_dev.h"
 #include "topk_dev.h"
 
