@@ -114,3 +114,75 @@ def test_step_captured():
         for s, got in zip((st, other), seen):
             for a, b in zip(got, s.run()):
                 assert torch.equal(a, b), i
+
+
+def far(rows, width, gap):
+    """[rows, width] of bf16 whose last row lies past 2^31 elements."""
+    t = torch.empty((rows - 1) * gap + width, dtype=torch.bfloat16, device=DEV)
+    assert (rows - 1) * gap > 2 ** 31
+    return t.as_strided((rows, width), (gap, 1))
+
+
+@pytest.mark.parametrize("rows", [3, 2100])
+def test_rows_far_apart(rows):
+    """Offsets past 32 bits: the results are those of the rows side by side."""
+    rs = np.random.default_rng(rows)
+    gap = 2 ** 31 // (rows - 1) + 64
+    wide = far(rows, 512, gap)
+    near = th.rnd(rs, (rows, 512), torch.bfloat16)
+    wide.copy_(near)
+    pos = torch.arange(rows, device=DEV)
+    table, w = moeq.rope_table(rows, 64), th.rnd(rs, (64,), torch.bfloat16)
+    parts = lambda t: t.unflatten(1, (8, 64))  # noqa: E731
+    want, _ = moeq.head_norm_rope(parts(near), None, w, pos=pos, table=table)
+    got, _ = moeq.head_norm_rope(parts(wide), None, w, pos=pos, table=table)
+    assert torch.equal(got, want)
+    ids = torch.from_numpy(rs.integers(0, 512, rows)).to(DEV)
+    for a, b in zip(moeq.token_logprobs(wide, ids, top=3), moeq.token_logprobs(near, ids, top=3)):
+        assert torch.equal(a, b)
+    s, _ = ta.make(rs, 2, 64, 512, 512, torch.bfloat16)
+    plan = moeq.adapter_plan(torch.from_numpy(rs.integers(-1, 2, rows).astype(np.int32)).to(DEV), 2)
+    want = moeq.add_adapters(s, near, plan, near, out=torch.empty_like(near))
+    assert torch.equal(moeq.add_adapters(s, wide, plan, wide, out=torch.empty_like(near)), want)
+    out = far(rows, 512, gap)
+    assert torch.equal(moeq.add_adapters(s, near, plan, near, out=out), want)
+    # heads in place, their rows far apart
+    moeq.head_norm_rope(parts(wide), None, w, pos=pos, table=table, q_out=parts(wide))
+    assert torch.equal(parts(wide), moeq.head_norm_rope(parts(near), None, w, pos=pos, table=table)[0])
+
+
+def test_two_streams_at_once():
+    """Calls in flight together on one set, plan and table, each with its own workspace."""
+    rs = np.random.default_rng(3)
+    T, K = 2100, 512
+    s, _ = ta.make(rs, 3, 64, K, K, torch.bfloat16)
+    plan = moeq.adapter_plan(torch.from_numpy(rs.integers(-1, 3, T).astype(np.int32)).to(DEV), 3)
+    xs = [th.rnd(rs, (T, K), torch.bfloat16) for _ in range(2)]
+    ids = torch.from_numpy(rs.integers(0, K, T)).to(DEV)
+    run = lambda x: [moeq.add_adapters(s, x, plan, x, out=torch.empty_like(x)),  # noqa: E731
+                     *moeq.token_logprobs(x, ids, top=4)]
+    want = [run(x) for x in xs]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in xs]
+    got = [[], []]
+    for _ in range(5):
+        for i, (x, stream) in enumerate(zip(xs, streams)):
+            with torch.cuda.stream(stream):
+                got[i].append(run(x))
+    torch.cuda.synchronize()
+    for w, runs in zip(want, got):
+        for r in runs:
+            for a, b in zip(r, w):
+                assert torch.equal(a, b)
+
+
+def test_space_of_a_larger_batch():
+    """A workspace and a plan's bytes made for the largest batch serve the smaller ones."""
+    rs = np.random.default_rng(4)
+    s, _ = ta.make(rs, 2, 64, 300, 100, torch.bfloat16)
+    ws = moeq.add_adapters_workspace(s, 4096)
+    for T in (1, 1000, 1023, 1024, 2047, 2048, 4096):
+        x, y = th.rnd(rs, (T, 300), torch.bfloat16), th.rnd(rs, (T, 100), torch.bfloat16)
+        plan = moeq.adapter_plan(torch.from_numpy(rs.integers(-1, 2, T).astype(np.int32)).to(DEV), 2)
+        want = moeq.add_adapters(s, x, plan, y, out=torch.empty_like(y))
+        assert torch.equal(moeq.add_adapters(s, x, plan, y, out=torch.empty_like(y), ws=ws), want)
