@@ -12,9 +12,9 @@
 // log2(G) lane steps and no workgroup barrier; a wave holds 64 / G heads of one token.
 //
 // HBM bounds large batches: 4096 tokens of 64 + 8 heads of 128 in bf16 move 151 MB in
-// 32 us (4.7 TB/s; a plain copy reaches 5.2 to 5.8).  A wave with several steps of heads,
-// which read the table's row and the weights once, was no faster (2 / 4 / 8 steps: 32.9 /
-// 33.1 / 39 us).  One token is a launch and the chain position -> table -> rotation: 3.8 us.
+// 30 us (5.0 TB/s; a plain copy reaches 5.1 to 5.8).  A wave with several steps of heads,
+// which read the table's row and the weights once, was no faster (1 / 2 / 4 / 8 steps:
+// 32 / 32.9 / 33.1 / 39 us).  One token is a launch and the chain position -> table -> rotation: 3.6 us.
 #include <type_traits>
 
 #include "elem_dev.h"
