@@ -280,10 +280,11 @@ __global__ __launch_bounds__(kThreads, DT == MOE_DT_F32 ? 4 : 8) void k_slice(Lo
     // ------------------------------------------------ the sums
     // z = x k - m k in one instruction.  What m k loses in its rounding (under 2^-4) is the
     // same for every term of the slice and put back at the end; past 2^20 it could be more
-    // than an exponent holds, and z is (x - m) k.
+    // than an exponent holds, and z is (x - m) k.  Terms whose z is -inf, as a masked one's is
+    // or may overflow to, have p = 0 and add nothing to d: a wave that may hold one bounds z.
     const float k = scale_of(P, t) * 1.44269504088896340736f;
     const float mk = m * k, rest = __builtin_fmaf(m, k, -mk);
-    const bool far = !(fabsf(mk) < 0x1p20f), masked = __any(least < -0x1p90f);
+    const bool far = !(fabsf(mk) < 0x1p20f), low = __any(!(least * k > -0x1p100f));
     float s = 0.f, d = 0.f;
     auto sums = [&](auto plain) {
         constexpr bool PLAIN = decltype(plain)::value;
@@ -296,12 +297,12 @@ __global__ __launch_bounds__(kThreads, DT == MOE_DT_F32 ? 4 : 8) void k_slice(Lo
                 float z = PLAIN || !far ? __builtin_fmaf(v, k, -mk) : (v - m) * k;
                 const float p = __builtin_amdgcn_exp2f(z);
                 s += p;
-                if constexpr (!PLAIN) z = fmaxf(z, -0x1p100f);     // a masked one: 0 * -inf
+                if constexpr (!PLAIN) z = fmaxf(z, -0x1p100f);     // 0 * -inf
                 d = __builtin_fmaf(p, z, d);
             }
         }
     };
-    if (far || masked) sums(std::false_type{});
+    if (far || low) sums(std::false_type{});
     else sums(std::true_type{});
     s = all_sum(s);
     d = all_sum(d);
@@ -419,7 +420,7 @@ __global__ __launch_bounds__(FLAT ? kFlat : 64) void k_join(LogArgs A) {
     }
     s = all_sum(s);
     d = all_sum(d);
-    const bool bad = !(s >= 0.f);
+    const bool bad = !(s >= 0.f) || d != d;
     const float logS = logf(s);
     auto logprob = [&](float x) {
         if (bad || x != x) return NaN;
