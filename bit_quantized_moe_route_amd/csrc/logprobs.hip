@@ -50,6 +50,18 @@ __device__ __forceinline__ float scale_of(const moe_logprobs& P, int64_t t) {
     return s > 0.f && s < __builtin_inff() ? s : __uint_as_float(0x7fc00000u);
 }
 
+// The scale in units of log2 e.  Past 2^128 / log2 e that leaves fp32's range where the scale
+// does not: k is half of it, and an exponent k times its difference twice that.
+struct ScaleLog2 {
+    float k, twice;
+    __device__ __forceinline__ explicit ScaleLog2(float s)
+        : k(s * 1.44269504088896340736f), twice(1.f) {
+        if (k < __builtin_inff()) return;
+        k = 0.5f * s * 1.44269504088896340736f;
+        twice = 2.f;
+    }
+};
+
 // A logit's order: 0 for the masked ones (-inf; NaN too), which no list holds.
 __device__ __forceinline__ uint32_t order_of(float x) {
     return x > -__builtin_inff() ? mono_bits(x) : 0u;
@@ -280,11 +292,14 @@ __global__ __launch_bounds__(kThreads, DT == MOE_DT_F32 ? 4 : 8) void k_slice(Lo
     // ------------------------------------------------ the sums
     // z = x k - m k in one instruction.  What m k loses in its rounding (under 2^-4) is the
     // same for every term of the slice and put back at the end; past 2^20 it could be more
-    // than an exponent holds, and z is (x - m) k.  Terms whose z is -inf, as a masked one's is
-    // or may overflow to, have p = 0 and add nothing to d: a wave that may hold one bounds z.
-    const float k = scale_of(P, t) * 1.44269504088896340736f;
+    // than an exponent holds, and z is (x - m) k, as it is for the largest scales.  Terms
+    // whose z is -inf, as a masked one's is or may overflow to, have p = 0 and add nothing to
+    // d: a wave that may hold one bounds z.
+    const ScaleLog2 scale(scale_of(P, t));
+    const float k = scale.k, twice = scale.twice;
     const float mk = m * k, rest = __builtin_fmaf(m, k, -mk);
-    const bool far = !(fabsf(mk) < 0x1p20f), low = __any(!(least * k > -0x1p100f));
+    const bool far = !(fabsf(mk) < 0x1p20f) || twice != 1.f;
+    const bool low = __any(!(least * k > -0x1p100f));
     float s = 0.f, d = 0.f;
     auto sums = [&](auto plain) {
         constexpr bool PLAIN = decltype(plain)::value;
@@ -294,7 +309,7 @@ __global__ __launch_bounds__(kThreads, DT == MOE_DT_F32 ? 4 : 8) void k_slice(Lo
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
                 const float v = elem_of<DT>(x[c], e);
-                float z = PLAIN || !far ? __builtin_fmaf(v, k, -mk) : (v - m) * k;
+                float z = PLAIN || !far ? __builtin_fmaf(v, k, -mk) : (v - m) * k * twice;
                 const float p = __builtin_amdgcn_exp2f(z);
                 s += p;
                 if constexpr (!PLAIN) z = fmaxf(z, -0x1p100f);     // 0 * -inf
@@ -408,13 +423,15 @@ __global__ __launch_bounds__(FLAT ? kFlat : 64) void k_join(LogArgs A) {
     };
     // the given tokens' logits are on their way before the slices are joined
     const float given = lane < P.m ? logit_of(id_of(lane)) : 0.f;
-    const float sc = scale_of(P, t), k = sc * 1.44269504088896340736f;
+    const float sc = scale_of(P, t);
+    const ScaleLog2 scale(sc);
     const float M = all_max(in ? st.max : -inf);
     const bool empty = M == -inf;
     float s = 0.f, d = 0.f;
     if (in) {
         // a slice of masked logits has S = 0; NaN of any slice stays
-        const float z = st.max > -inf ? (st.max - M) * k : 0.f, f = __builtin_amdgcn_exp2f(z);
+        const float z = st.max > -inf ? (st.max - M) * scale.k * scale.twice : 0.f;
+        const float f = __builtin_amdgcn_exp2f(z);
         s = st.sum * f;
         d = f * (st.dot + fmaxf(z, -0x1p100f) * st.sum);
     }

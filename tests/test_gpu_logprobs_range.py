@@ -49,6 +49,21 @@ def check(x, scale, ids, top):
     close(got[3], want, tol(want), "best log p")
 
 
+@pytest.mark.parametrize("dt", sorted(TYPES))
+def test_scales_up_to_the_largest(dt):
+    """Scales that leave fp32's range once they are in units of log2 e are scales like any other:
+    logits that lie a few parts of 2^-127 apart (fp16: the next one is 2^-24 off, and has
+    no probability left)."""
+    say("largest scales", dt)
+    rs = np.random.default_rng(21)
+    unit = 2.0 ** -24 if dt == "fp16" else 2.0 ** -127
+    scales = (1.0e38, 1.7e38, 2.35e38, 2.4e38, 3.0e38, LARGEST)
+    steps = rs.integers(0, 9, (len(scales), V))
+    steps[1::2, :16384] += 1                # the largest in the second slice alone
+    x = torch.from_numpy(-steps * unit).to(TYPES[dt]).to(DEV)
+    check(x, scales, [0, 16383, 16384, V - 1], 12)
+
+
 @pytest.mark.parametrize("dt,low,high,scale", [
     ("fp32", -6.0, 0.0, 1.2e38), ("bf16", -6.0, 0.0, 1.2e38), ("fp16", -6.0, 0.0, 1.2e38),
     ("fp32", -1e27, 0.0, 1e12), ("bf16", -1e27, 0.0, 1e12), ("fp16", -65504.0, 0.0, 1e35),
