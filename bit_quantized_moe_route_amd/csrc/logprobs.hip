@@ -62,6 +62,12 @@ struct ScaleLog2 {
     }
 };
 
+// (x - M) k of x <= M, both finite, also where the difference leaves fp32's range.
+__device__ __forceinline__ float diff_times(float x, float M, float k) {
+    const float d = x - M;
+    return d > -__builtin_inff() ? d * k : (0.5f * x - 0.5f * M) * k * 2.f;
+}
+
 // A logit's order: 0 for the masked ones (-inf; NaN too), which no list holds.
 __device__ __forceinline__ uint32_t order_of(float x) {
     return x > -__builtin_inff() ? mono_bits(x) : 0u;
@@ -430,7 +436,7 @@ __global__ __launch_bounds__(FLAT ? kFlat : 64) void k_join(LogArgs A) {
     float s = 0.f, d = 0.f;
     if (in) {
         // a slice of masked logits has S = 0; NaN of any slice stays
-        const float z = st.max > -inf ? (st.max - M) * scale.k * scale.twice : 0.f;
+        const float z = st.max > -inf ? diff_times(st.max, M, scale.k) * scale.twice : 0.f;
         const float f = __builtin_amdgcn_exp2f(z);
         s = st.sum * f;
         d = f * (st.dot + fmaxf(z, -0x1p100f) * st.sum);
@@ -441,7 +447,7 @@ __global__ __launch_bounds__(FLAT ? kFlat : 64) void k_join(LogArgs A) {
     const float logS = logf(s);
     auto logprob = [&](float x) {
         if (bad || x != x) return NaN;
-        return empty || x == -inf ? -inf : (x - M) * sc - logS;
+        return empty || x == -inf ? -inf : diff_times(x, M, sc) - logS;
     };
     if (tid == 0 && P.entropy)
         P.entropy[t] = bad ? NaN : empty ? 0.f : fmaxf(logS - 0.69314718055994530942f * (d / s), 0.f);

@@ -80,3 +80,17 @@ def test_scaled_logits_that_overflow(dt, low, high, scale):
     x[2, 8] = high - 1 / scale
     x[3, 19999] = high                      # a slice of low ones, and one with the largest
     check(x, [scale] * 4, [0, 7, 8, 17000, 19999], 3)
+
+
+@pytest.mark.parametrize("dt", ["bf16", "fp32"])
+def test_differences_that_overflow(dt):
+    """Logits that lie further apart than fp32's largest value, at scales that bring them
+    together again.  (3e-40 is held to 2^-150 as a factor of differences up to 2^129, so
+    to 2^-21 of an exponent: under the tolerance's 24 parts of 2^-22.)"""
+    say("differences", dt)
+    rs = np.random.default_rng(22)
+    x = torch.from_numpy(rs.integers(-3, 4, (10, V)) * 1e38).to(TYPES[dt]).to(DEV)
+    x[5:, :16384] = -3e38                   # a slice apart from the largest
+    x[5:, 19000] = 3e38
+    scales = [2e-38, 3e-40, 1e-37, 1e-30, 1e-4] * 2
+    check(x, scales, [0, 5, 16384, 18000, 19000], 8)
