@@ -13,9 +13,10 @@
 //
 // Both products are matrix instructions on 16-bit operands with fp32 sums.  x and the
 // weights are 16-bit as they are (8-bit codes are exact in either type).  h stays fp32-like:
-// it enters the second product as the sum of two numbers of the weights' type.  fp16 holds
-// 22 bits of h so, its row first brought to [1, 2) by a power of two; bf16 16 bits, enough
-// for a 16-bit result, and a third number follows where y is fp32.
+// it enters the second product as the sum of two numbers of the weights' type.  bf16 holds
+// 16 bits of h so, enough for a 16-bit result, and a third number follows where y is fp32.
+// fp16 holds 22 bits, down to its smallest step of 2^-24: so a token's row of h first goes to
+// a largest of [2^14, 2^15) by a power of two, and what is 2^-17 of that still has its 22.
 //
 // Few tokens are bound by latency: one token, 6144 -> 6144, rank 16: 3.3 and 3.8 us for the
 // two; 64 tokens and as many slots of ranks to 64, 6144 -> 2048: 7.6 and 4.7.  4096 tokens,
@@ -243,6 +244,9 @@ __global__ __launch_bounds__(64 * kAdWaves) void k_shrink(AdArgs A) {
                               (lane >> 4) * 4) = v * S.scales[a];
 }
 
+// fp16's power of two for a row of h, from the bits of its largest.
+__device__ __forceinline__ int exponent_h(uint32_t most) { return (int)(most >> 23) - 127 - 14; }
+
 // h (four ranks of a token) as the operand of the second product: two numbers each, in h3
 // the third.  ex: fp16's power of two.
 template <bool BF>
@@ -334,7 +338,7 @@ __global__ __launch_bounds__(32 * kSlots, 2) void k_shrink_wide(AdArgs A) {
         if (r >= rts) continue;
         int ex = 0;
         if constexpr (!BF) {
-            ex = (int)(most[16 * m + (l & 15)] >> 23) - 127;
+            ex = exponent_h(most[16 * m + (l & 15)]);
             if (r == 0 && l < 16) A.hf[(piece * M + m) * 16 + l] = ldexpf(1.f, ex);
         }
         uint2 h3;
@@ -483,7 +487,7 @@ __global__ __launch_bounds__(64 * kAdWaves, 2) void k_expand(AdArgs A) {
         for (int i = 0; i < NI; ++i) m = max(m, max_bits(v[i]));
         atomicMax(&most[lane & 15], m);
         __syncthreads();
-        ex = (int)(most[lane & 15] >> 23) - 127;
+        ex = exponent_h(most[lane & 15]);
         f = ldexpf(1.f, ex);
     }
 #pragma unroll
