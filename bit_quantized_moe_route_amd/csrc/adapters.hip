@@ -255,8 +255,11 @@ __device__ __forceinline__ u32x4 split_h(f32x4 v, int ex, uint2& h3) {
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
         if constexpr (BF) {
-            lo[e] = v[e] - (float)(__bf16)v[e];
+            // what would round past bf16's largest stays there, and the rest is in lo
+            const float hi = __builtin_amdgcn_fmed3f(v[e], -0x1.fep127f, 0x1.fep127f);
+            lo[e] = v[e] - (float)(__bf16)hi;
             lo3[e] = lo[e] - (float)(__bf16)lo[e];
+            v[e] = hi;
         } else {
             v[e] = ldexpf(v[e], -ex);
             lo[e] = v[e] - (float)(_Float16)v[e];

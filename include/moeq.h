@@ -853,9 +853,9 @@ int moe_adapter_plan(const int32_t* ids, int64_t T, int32_t n, void* plan, size_
  *   y, out     [device] [T, N] of y_dtype (F32, BF16, F16), rows ldy and ldo apart; out may
  *              be y itself (with its stride), else it overlaps no operand.
  *   workspace  [device] >= moe_add_adapters_workspace_bytes(), 256-byte aligned.
- *   s A x enters the second product rounded: of bf16 adapters to 2^-16 of itself, or 2^-24
- *   where y_dtype is F32; of fp16 ones to 2^-22 of itself or 2^-39 of the token's largest,
- *   whichever is more.  An infinity or NaN of x touches its own token only.  A token's bits
+ *   s A x enters the second product rounded: of bf16 adapters to 2^-16 of itself, 2^-24 where
+ *   y_dtype is F32, or to 2^-134; of fp16 ones to 2^-22 of itself or 2^-39 of the token's
+ *   largest (whichever is more).  An infinity or NaN of x touches its own token only.  A token's bits
  *   depend on its row and its adapter alone.
  */
 size_t moe_add_adapters_workspace_bytes(const moe_adapters* set, int64_t T);

@@ -51,3 +51,63 @@ def test_ranks_of_different_size(T, rank, K, N, y):
     tol = tol * (1 + half) + (half + 2.0 ** -24) * np.abs(ref) + TINY[rows.dtype]
     err = np.abs(f64(got) - ref)
     assert np.all(err <= tol), float((err / tol).max())
+
+
+@pytest.mark.parametrize("w", ["bf16", "fp16"])
+@pytest.mark.parametrize("T", [5, 4200])
+@pytest.mark.parametrize("e", [-118, -105, 100, 120])
+def test_scales_far_from_one(e, T, w):
+    """s A x near both ends of fp32's range, and results that return to its middle.  Numbers of
+    fp32 below 2^-126 are off by 2^-150 a rounding (under 32 of them in h), those of bf16 by
+    2^-134."""
+    say("far scales", e, T, w)
+    rs = np.random.default_rng(T)
+    rank, K, N, n = 32, 96, 70, 2
+    s, known = moeq.Adapters(n, rank, K, N, dtype=TYPES[w]), []
+    back = -e if w == "bf16" else (12 if e < 0 else -12)
+    for i in range(n):
+        a = torch.from_numpy(rs.standard_normal((rank, K)) / 8).to(TYPES[w]).to(DEV)
+        b = torch.from_numpy(rs.standard_normal((N, rank)) * 2.0 ** back).to(TYPES[w]).to(DEV)
+        s.load(i, a, b, 2.0 ** e)
+        known.append((f64(a), f64(b), np.float32(2.0 ** e)))
+    ids = rs.integers(0, n, T).astype(np.int32)
+    x = torch.from_numpy(rs.standard_normal((T, K))).to(TYPES[w]).to(DEV)
+    y = torch.zeros((T, N), device=DEV)
+    got = moeq.add_adapters(s, x, moeq.adapter_plan(torch.from_numpy(ids).to(DEV), n), y,
+                            out=torch.empty_like(y))
+    ref, bh, bax, bmax = op.add_adapters(f64(x), ids, known, f64(y))
+    split = 2.0 ** -24 * bh if w == "bf16" else 2.0 ** -22 * bh + 2.0 ** -39 * bmax
+    small = 2.0 ** -145 + (2.0 ** -134 if w == "bf16" else 0)
+    absb = np.stack([np.abs(k[1]).sum(1) for k in known])[ids]
+    tol = 2.0 ** -23 * ((K / 16 + 152) * bax + (3 * rank + 8) * bh) + split + small * absb
+    tol = tol * (1 + 2.0 ** -24) + 2.0 ** -23 * np.abs(ref) + 2.0 ** -149
+    err = np.abs(f64(got) - ref)
+    assert np.all(err <= tol), float((err / tol).max())
+
+
+@pytest.mark.parametrize("w", ["bf16", "fp16"])
+@pytest.mark.parametrize("T,rank", [(3, 1), (4200, 32)])
+@pytest.mark.parametrize("y", ["fp32", "bf16"])
+def test_the_largest_values(T, rank, y, w):
+    """s A x between the largest number of bf16 and that of fp32 is a number like any other."""
+    say("largest", T, rank, y, w)
+    K, N = 40, 70
+    s = moeq.Adapters(1, rank, K, N, dtype=TYPES[w])
+    a, b = (torch.zeros(shape, dtype=TYPES[w], device=DEV) for shape in ((rank, K), (N, rank)))
+    a[0, 3] = 1.0
+    b[:, 0] = 2.0 ** -10 * (torch.arange(N, device=DEV) % 7 - 3)
+    scale = float(np.float32(3.3975e38))
+    s.load(0, a, b, scale)
+    x = torch.zeros((T, K), dtype=TYPES[w], device=DEV)
+    x[:, 3] = 1.0
+    x[1::2, 3] = -1.0
+    rows = torch.zeros((T, N), dtype=TYPES[y], device=DEV)
+    got = moeq.add_adapters(s, x, moeq.adapter_plan(torch.zeros(T, dtype=torch.int32, device=DEV), 1),
+                            rows, out=torch.empty_like(rows))
+    ref = f64(x)[:, 3:4] * scale * f64(b)[:, 0]
+    # one product: the split's 2^-24 (bf16, fp32 results), 2^-16 (bf16) or 2^-22 of h, two
+    # roundings of fp32 and one of y
+    split = 2.0 ** -22 if w == "fp16" else 2.0 ** -24 if y == "fp32" else 2.0 ** -16
+    tol = (split + 2.0 ** -22 + torch.finfo(rows.dtype).eps / 2) * np.abs(ref)
+    err = np.abs(f64(got) - ref)
+    assert np.all(err <= tol), float((err / np.maximum(tol, 1e-300)).max())
