@@ -117,6 +117,8 @@ int launch_permute(const int32_t* ids, int64_t T, int32_t k, int32_t E,
                    int32_t* counts, int32_t* offsets, int32_t* perm_src,
                    int32_t* inv_perm, void* ws, void* stream);
 size_t permute_ws_bytes(int64_t T, int32_t k, int32_t E);
+// As many or more, and never fewer for more tokens.
+size_t permute_ws_most_bytes(int64_t T, int32_t k, int32_t E);
 bool route_permute_fused_ok(int64_t T, int32_t k);
 int launch_route_permute(const float* logits, int64_t T, int32_t E, int32_t k, int32_t* ids,
                          float* w, int32_t* counts, int32_t* offsets, int32_t* perm_src,
@@ -303,7 +305,7 @@ inline AdPlan ad_plan(int64_t T, int32_t n, int tile) {
     p.offsets = p.counts + round_up(n + 1, 4);
     p.inv = p.offsets + round_up(n + 2, 4);
     p.ws = p.inv + round_up(T, 4);
-    p.total = p.ws + (int64_t)permute_ws_bytes(T, 1, n + 1) / 4;
+    p.total = p.ws + (int64_t)permute_ws_most_bytes(T, 1, n + 1) / 4;
     return p;
 }
 inline AdPlan ad_plan(int64_t T, int32_t n) {

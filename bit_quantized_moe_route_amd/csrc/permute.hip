@@ -351,6 +351,14 @@ size_t permute_ws_bytes(int64_t T, int32_t k, int32_t E) {
     return (size_t)(nb * E) * sizeof(int32_t);
 }
 
+// (A slice grows by whole rounds of threads, so their number falls now and then.)
+size_t permute_ws_most_bytes(int64_t T, int32_t k, int32_t E) {
+    const int64_t n = T * k;
+    if (permute_single(n)) return 0;
+    const int64_t nb = (n + kPermSlice - 1) / kPermSlice;
+    return (size_t)((nb < kPermMaxSlices ? nb : kPermMaxSlices) * E) * sizeof(int32_t);
+}
+
 int launch_permute(const int32_t* ids, int64_t T, int32_t k, int32_t E, int32_t* counts,
                    int32_t* offsets, int32_t* perm_src, int32_t* inv_perm, void* ws,
                    void* stream) {

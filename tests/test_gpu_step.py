@@ -186,3 +186,27 @@ def test_space_of_a_larger_batch():
         plan = moeq.adapter_plan(torch.from_numpy(rs.integers(-1, 2, T).astype(np.int32)).to(DEV), 2)
         want = moeq.add_adapters(s, x, plan, y, out=torch.empty_like(y))
         assert torch.equal(moeq.add_adapters(s, x, plan, y, out=torch.empty_like(y), ws=ws), want)
+
+
+@pytest.mark.parametrize("n", [3, 1000])
+def test_plans_in_the_bytes_of_a_larger_one(n):
+    """The bytes of a larger batch's plan, and its workspace, take any smaller batch's; nothing
+    behind them is written.  (At 131073 tokens the sort goes on to fewer slices.)"""
+    rs = np.random.default_rng(n)
+    most = 131073
+    s, _ = ta.make(rs, n, 3, 16, 8, torch.bfloat16)
+    L = moeq.lib()
+    size = L.moe_adapter_plan_bytes(most, n)
+    ws = moeq.add_adapters_workspace(s, most)
+    ids = torch.from_numpy(rs.integers(-1, n, most).astype(np.int32)).to(DEV)
+    x, y = th.rnd(rs, (most, 16), torch.bfloat16), th.rnd(rs, (most, 8), torch.bfloat16)
+    for T in (most, 131072, 100000, 4097, 4096, 1024, 1):
+        data = torch.full((size + 64,), 77, dtype=torch.uint8, device=DEV)
+        stream = torch.cuda.current_stream().cuda_stream
+        assert L.moe_adapter_plan(ids.data_ptr(), T, n, data.data_ptr(), size, stream) == 0
+        assert (data[size:] == 77).all()
+        got = moeq.add_adapters(s, x[:T], moeq.AdapterPlan(T, n, data), y[:T],
+                                out=torch.empty_like(y[:T]), ws=ws)
+        want = moeq.add_adapters(s, x[:T], moeq.adapter_plan(ids[:T].clone(), n), y[:T],
+                                 out=torch.empty_like(y[:T]))
+        assert torch.equal(got, want), T

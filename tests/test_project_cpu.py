@@ -265,6 +265,25 @@ def test_bytes_never_fall_with_the_tokens(n, rank, K):
     assert plans == sorted(plans) and spaces == sorted(spaces)
 
 
+@pytest.mark.parametrize("n", [1, 8, 64, 300, 1023])
+def test_bytes_never_fall_where_the_sort_changes(n):
+    """Around the token counts at which the sort of a large plan, its tiles or the dispatch of
+    the products change: multiples of 65536 and of 32 slots, and sizes spread up to 2^31."""
+    s = ma.AdaptersC(n=n, rank=64, K=6144, N=64)
+    Ts = {(1 << 31) - 4097}
+    for base in [*range(0, 20 << 16, 1 << 16), 1024, 4096, 32 * n, *(1 << i for i in range(21, 31))]:
+        Ts.update(range(max(1, base - 3), base + 4))
+    T = 1
+    while T < (1 << 31) - 4096:
+        Ts.add(T)
+        T += T // 97 + 1
+    Ts = sorted(Ts)
+    L = moeq.lib()
+    plans = [L.moe_adapter_plan_bytes(T, n) for T in Ts]
+    spaces = [L.moe_add_adapters_workspace_bytes(ctypes.byref(s), T) for T in Ts]
+    assert plans[0] and plans == sorted(plans) and spaces == sorted(spaces)
+
+
 def test_plan_refusals():
     for T, n in ((-1, 1), (1, 0), (1, 1024), (1 << 31, 1)):
         refused("moe_adapter_plan", P, T, n, P, 1 << 20, None)
