@@ -322,3 +322,31 @@ def test_beside_an_8_bit_product(T, K, N):
             moeq.linear_i8(lin, x, **kw)
     with pytest.raises(ValueError, match="adapters"):
         moeq.linear_i8(lin, x.half(), adapters=s, plan=plan)
+
+
+@pytest.mark.parametrize("w", [torch.bfloat16, torch.float16])
+@pytest.mark.parametrize("codes", [False, True])
+@pytest.mark.parametrize("T,rank,K", [(4100, 32, 1300), (2100, 60, 3000), (2800, 48, 130), (1030, 128, 700),
+                                      (1700, 80, 2100), (1100, 130, 520), (2050, 16, 400)])
+def test_bits_in_every_kernel(T, rank, K, codes, w):
+    """The same bits for a token alone, in a few and among many, at every set of kernels that the
+    dispatch takes for the batch: rows and codes, ranks to 32, 64 and 128, more, and 16."""
+    say("bits", T, rank, K, codes, w)
+    rs = np.random.default_rng(T + rank)
+    n, N = 4, 136
+    s, _ = make(rs, n, rank, K, N, w, ranks=[rank, rank // 3, rank - 1, 5])
+    ids = torch.from_numpy(rs.integers(-1, n, T).astype(np.int32)).to(DEV)
+    x, scale = rnd(rs, (T, K), w), None
+    if codes:
+        x, scale = moeq.quantize_i8(x)
+    for yt in (torch.float32, w):
+        y = rnd(rs, (T, N), yt)
+
+        def run(a, b):
+            return moeq.add_adapters(s, x[a:b], moeq.adapter_plan(ids[a:b].clone(), n), y[a:b],
+                                     scale=None if scale is None else scale[a:b].clone(),
+                                     out=torch.empty_like(y[a:b]))
+
+        whole = run(0, T)
+        for a, b in ((0, 1), (77, 78), (T - 1, T), (500, 590), (0, 1000)):
+            assert torch.equal(run(a, b), whole[a:b]), (a, b)
