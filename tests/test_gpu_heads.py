@@ -230,3 +230,24 @@ def test_stream_and_graph():
         torch.cuda.synchronize()
         want = moeq.head_norm_rope(q, k, w, w, pos=pos, table=table)
         assert torch.equal(qo, want[0]) and torch.equal(ko, want[1]), i
+
+
+@pytest.mark.parametrize("dt", sorted(TYPES))
+@pytest.mark.parametrize("inter", [False, True])
+@pytest.mark.parametrize("T,Hq,Hk,D,R", [(520, 28, 4, 128, 128), (700, 12, 4, 192, 64),
+                                         (9000, 3, 0, 80, 16)])
+def test_results_past_the_caches(T, Hq, Hk, D, R, inter, dt):
+    """2^21 elements and more, whose results go past the caches."""
+    say("large", T, Hq, Hk, D, R, inter, dt)
+    assert T * (Hq + Hk) * D >= 2 ** 21 and D % 16 == 0 and R % 16 == 0
+    rs = np.random.default_rng(T)
+    q = rnd(rs, (T, Hq, D), TYPES[dt], 3.0)
+    k = rnd(rs, (T, Hk, D), TYPES[dt]) if Hk else None
+    qw, kw = rnd(rs, (D,), TYPES[dt]), rnd(rs, (D,), TYPES[dt]) if Hk else None
+    pos = rs.integers(0, 3000, T)
+    c, s = cos_sin(pos, R, 3000)
+    outs = moeq.head_norm_rope(q, k, qw, kw, pos=torch.from_numpy(pos).to(DEV),
+                               table=moeq.rope_table(3000, R), interleaved=inter)
+    for x, w, o in ((q, qw, outs[0]), (k, kw, outs[1])):
+        if x is not None:
+            close(o, *op.heads(f64(x), f64(w), 1e-5, 0.0, c, s, inter), "norm and rotation")

@@ -259,3 +259,26 @@ def test_stream_and_graph():
         torch.cuda.synchronize()
         for a, b in zip(moeq.token_logprobs(x, ids, top=7), list(out.values())):
             assert torch.equal(a, b), i
+
+
+@pytest.mark.parametrize("dt", sorted(TYPES))
+@pytest.mark.parametrize("top", [0, 8])
+def test_more_logits_than_the_caches_hold(top, dt):
+    """2^28 bytes of logits and more, which are read past the caches: rows among them against the
+    oracle, and all of them bit for bit as in batches that are not."""
+    say("large", top, dt)
+    V = 50257
+    T = 2 ** 28 // (V * (4 if dt == "fp32" else 2)) + 2
+    g = torch.Generator(device=DEV).manual_seed(5)
+    x = torch.randn((T, V), generator=g, device=DEV).mul_(3).to(TYPES[dt])
+    x[T // 2, ::5] = -float("inf")
+    ids = torch.randint(0, V, (T, 2), generator=g, device=DEV, dtype=torch.int32)
+    whole = moeq.token_logprobs(x, ids, top=top)
+    half = T // 2 + 1
+    for a, b in ((0, half), (half, T)):
+        for u, v in zip(moeq.token_logprobs(x[a:b], ids[a:b], top=top), whole):
+            assert torch.equal(u, v[a:b])
+    some = [0, T // 2, T - 1]
+    got = check(x[some], top, ids[some])
+    for u, v in zip(got, whole):
+        assert torch.equal(u, v[some])
