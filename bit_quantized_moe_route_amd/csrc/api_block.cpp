@@ -11,7 +11,6 @@ using namespace moeq;
 namespace {
 
 constexpr int32_t kMaxI8K = 131071;   // 2^31 / (128 * 128): int32 sums cannot wrap
-constexpr int32_t kMaxDim = 1 << 24;
 
 // The products' tiles are 128 rows by 256 channels wherever they are many, and
 // no smaller than 32 rows for up to 64 rows of each expert: the workgroups of a

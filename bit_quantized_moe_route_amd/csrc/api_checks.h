@@ -10,6 +10,7 @@ namespace moeq {
 
 constexpr size_t kAlign = 256;
 constexpr int64_t kMaxRows = (int64_t)1 << 31;   // grid rows of one launch
+constexpr int32_t kMaxDim = 1 << 24;             // widths
 
 inline size_t align_up(size_t v) { return (v + kAlign - 1) / kAlign * kAlign; }
 

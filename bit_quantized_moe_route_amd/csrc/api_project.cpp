@@ -10,7 +10,6 @@ using namespace moeq;
 
 namespace {
 
-constexpr int32_t kMaxDim = 1 << 24;
 constexpr int32_t kMaxHeads = 4096;
 
 // No two of the n1 x n2 runs of D elements, s1 and s2 apart, overlap.
