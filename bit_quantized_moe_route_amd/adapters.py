@@ -13,7 +13,7 @@ refuses tensors of several devices.
 
 import ctypes
 
-from . import _I32, _I64, _P, _torch, lib
+from . import MOE_EINVAL, MOE_EWORKSPACE, MoeError, _I32, _I64, _P, _torch, lib
 from .block import DT_I8, _call, _call_on, _cuda, _dt, _flat, _rows, _x, codes_width
 from .heads import _flat_on, _gpu, _type
 
@@ -126,6 +126,17 @@ def add_adapters_workspace(adapters, T):
     """Workspace of add_adapters for T tokens."""
     n = lib().moe_add_adapters_workspace_bytes(ctypes.byref(adapters.c()), T)
     return _torch().empty(max(n, 256), dtype=_torch().uint8, device=adapters.device)
+
+
+def check_workspace(adapters, T, ws):
+    """Refuses a workspace that add_adapters would refuse, in the same way."""
+    need = lib().moe_add_adapters_workspace_bytes(adapters.at, T)
+    size = ws.numel()
+    at = _flat_on(ws, "the workspace", size, adapters.index, _torch().uint8)
+    if T and size < need:
+        raise MoeError(MOE_EWORKSPACE, "moe_add_adapters", f"workspace needs {need} bytes")
+    if T and at % 256:
+        raise MoeError(MOE_EINVAL, "moe_add_adapters", "workspace must be 256-byte aligned")
 
 
 def add_adapters(adapters, x, plan, y, scale=None, out=None, ws=None):

@@ -384,8 +384,8 @@ def linear_i8(linear, x, scale=None, out=None, out_dtype=None, ws=None, adapters
     """x [T, K] times the matrix, in 8 bits: [T, N] of out_dtype (x's type, bf16
     for codes, by default).  x: float rows, coded in the call, or int8 codes
     from quantize_i8 or a block norm with their scale.  With adapters (Adapters of
-    the same K and N) and the batch's plan, add_adapters follows on the result,
-    which is rounded to its type before and after."""
+    the same K and N, x of their type or codes) and the batch's plan, add_adapters
+    follows on the result, which is rounded to its type before and after."""
     torch = _torch()
     dev = _cuda(x, "linear_i8")
     if dev != linear.device:
@@ -397,6 +397,10 @@ def linear_i8(linear, x, scale=None, out=None, out_dtype=None, ws=None, adapters
                 or x.dtype not in (adapters.dtype, torch.int8):
             raise ValueError("adapters must be of the matrix's K and N and x's device and type, "
                              "with the batch's plan")
+        from .adapters import add_adapters, check_workspace
+
+        if adapter_ws is not None:            # refused before the product writes
+            check_workspace(adapters, T, adapter_ws)
     elif plan is not None or adapter_ws is not None:
         raise ValueError("plan and adapter_ws go with adapters")
     px, dt, ldx, ps = _x(x, scale, linear.K, dev)
@@ -410,8 +414,6 @@ def linear_i8(linear, x, scale=None, out=None, out_dtype=None, ws=None, adapters
         _call("moe_linear_i8", dev, ctypes.byref(linear.c()), px, dt, ldx, ps, T, out.data_ptr(),
               _dt(out.dtype), ldo, _dptr(ws), ws.numel() if ws is not None else 0)
     if adapters is not None:
-        from .adapters import add_adapters
-
         add_adapters(adapters, x, plan, out, scale=scale, ws=adapter_ws)
     return out
 

@@ -210,3 +210,22 @@ def test_plans_in_the_bytes_of_a_larger_one(n):
         want = moeq.add_adapters(s, x[:T], moeq.adapter_plan(ids[:T].clone(), n), y[:T],
                                  out=torch.empty_like(y[:T]))
         assert torch.equal(got, want), T
+
+
+def test_a_refused_adapter_workspace_leaves_the_output():
+    """linear_i8 refuses the adapters' workspace before the product writes."""
+    rs = np.random.default_rng(6)
+    lin = moeq.I8Linear.quantized(th.rnd(rs, (100, 256), torch.float32))
+    s, _ = ta.make(rs, 2, 16, 256, 100, torch.bfloat16)
+    x = th.rnd(rs, (9, 256), torch.bfloat16)
+    plan = moeq.adapter_plan(torch.zeros(9, dtype=torch.int32, device=DEV), 2)
+    ws = moeq.add_adapters_workspace(s, 9)
+    want = moeq.linear_i8(lin, x, adapters=s, plan=plan)
+    assert torch.equal(moeq.linear_i8(lin, x, adapters=s, plan=plan, adapter_ws=ws), want)
+    out = torch.full((9, 100), 7.0, dtype=torch.bfloat16, device=DEV)
+    wide = torch.empty(ws.numel() + 256, dtype=torch.uint8, device=DEV)
+    for bad in (ws[:256], ws.float(), ws.cpu(), wide[1:]):
+        with pytest.raises((ValueError, moeq.MoeError), match="workspace"):
+            moeq.linear_i8(lin, x, out=out, adapters=s, plan=plan, adapter_ws=bad)
+    torch.cuda.synchronize()
+    assert (out == 7).all()
