@@ -61,6 +61,8 @@ class Adapters:
                             b=self.b.data_ptr(), ranks=self.ranks.data_ptr(),
                             scales=self.scales.data_ptr())
         self.at = ctypes.byref(self._c)
+        self.bytes = torch.uint8
+        self.space = None, 0        # a number of tokens and the workspace they need
 
     def load(self, slot, a, b, scale=1.0):
         """Puts A [r, K] and B [N, r] (of the set's type) with their scale into a
@@ -130,10 +132,12 @@ def add_adapters_workspace(adapters, T):
 
 def check_workspace(adapters, T, ws):
     """Refuses a workspace that add_adapters would refuse, in the same way."""
-    need = lib().moe_add_adapters_workspace_bytes(adapters.at, T)
-    size = ws.numel()
-    at = _flat_on(ws, "the workspace", size, adapters.index, _torch().uint8)
-    if T and size < need:
+    of, need = adapters.space
+    if of != T:
+        need = lib().moe_add_adapters_workspace_bytes(adapters.at, T)
+        adapters.space = T, need
+    at = _flat_on(ws, "the workspace", ws.numel(), adapters.index, adapters.bytes)
+    if T and ws.numel() < need:
         raise MoeError(MOE_EWORKSPACE, "moe_add_adapters", f"workspace needs {need} bytes")
     if T and at % 256:
         raise MoeError(MOE_EINVAL, "moe_add_adapters", "workspace must be 256-byte aligned")
