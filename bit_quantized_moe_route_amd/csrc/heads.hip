@@ -176,16 +176,21 @@ __global__ __launch_bounds__(256) void k_heads(HeadArgs A) {
         const bool far = !(ms >= 0x1p-100f && ms < __builtin_inff());
         float rstd = 1.f / sqrtf(ms);
         if (__any(far)) {
-            // 1 / sqrt(mean square + eps) of the head times k, where the squares leave
-            // fp32's range: 2^-80 past its top, 2^100 where squares that underflow might
-            // count.  v * k * rstd does not notice.
-            const float k = !far ? 1.f : ms < 1.f ? 0x1p100f : 0x1p-80f;
+            // Where the squares leave fp32's range, the head times k: 2^-80 past its top,
+            // 2^100 where squares that underflow might count.  v goes up before it meets its
+            // 1 / sqrt(mean square + eps), and down after it, so that neither end is lost.
+            const float up = far && ms < 1.f ? 0x1p100f : 1.f;
+            const float down = far && up == 1.f ? 0x1p-80f : 1.f, k = up * down;
             const float again = mean_square(k) + P.eps * k * k;
-            if (far) rstd = 1.f / sqrtf(again);
+            const float r = far ? 1.f / sqrtf(again) : 1.f;
+            if (far) rstd = 1.f;
 #pragma unroll
             for (int n = 0; n < NU; ++n)
 #pragma unroll
-                for (int e = 0; e < V; ++e) a[n][e] *= k, b[n][e] *= k;
+                for (int e = 0; e < V; ++e) {
+                    a[n][e] = a[n][e] * up * r * down;
+                    b[n][e] = b[n][e] * up * r * down;
+                }
         }
 #pragma unroll
         for (int n = 0; n < NU; ++n)

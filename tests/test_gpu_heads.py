@@ -251,3 +251,24 @@ def test_results_past_the_caches(T, Hq, Hk, D, R, inter, dt):
     for x, w, o in ((q, qw, outs[0]), (k, kw, outs[1])):
         if x is not None:
             close(o, *op.heads(f64(x), f64(w), 1e-5, 0.0, c, s, inter), "norm and rotation")
+
+
+@pytest.mark.parametrize("dt", ["bf16", "fp32"])
+@pytest.mark.parametrize("D,R", [(64, 32), (66, 2), (36, 36), (1003, 4)])
+def test_small_elements_of_far_heads(D, R, dt):
+    """Heads whose squares leave fp32's range hold elements far below the others: these keep
+    their accuracy (their norms are over 2^-126)."""
+    say("far heads", D, R, dt)
+    rs = np.random.default_rng(D)
+    T, Hq = 6, 3
+    # an element of 2^66 among ones of 2^-55; of 2^-60 among ones of 2^-145; mixed in a wave
+    big = np.array([2.0 ** 66, 1.0, 2.0 ** 100, 2.0 ** -60, 2.0 ** 66, 2.0 ** 40])[:, None, None]
+    rest = np.array([2.0 ** -55, 2.0 ** -100, 2.0 ** -20, 2.0 ** -120, 2.0 ** -50, 2.0 ** -70])[:, None, None]
+    x = rest * (1 + rs.random((T, Hq, D))) * rs.choice([-1, 1], (T, Hq, D))
+    x[:, :, D // 2:D // 2 + 2] = big * (1 + rs.random((T, Hq, 2)))
+    q = torch.from_numpy(x).to(TYPES[dt]).to(DEV)
+    w = (rnd(rs, (D,), torch.float32).abs() + 0.5).to(TYPES[dt])
+    pos = torch.arange(T, device=DEV) + 3
+    c, s = cos_sin(pos.cpu().numpy(), R, 16)
+    got, _ = moeq.head_norm_rope(q, None, w, pos=pos, table=moeq.rope_table(16, R), eps=0.0)
+    close(got, *op.heads(f64(q), f64(w), 0.0, 0.0, c, s), "far heads")
