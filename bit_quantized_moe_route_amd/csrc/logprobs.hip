@@ -147,6 +147,9 @@ __global__ __launch_bounds__(kThreads, DT == MOE_DT_F32 ? 4 : 8) void k_slice(Lo
     const int v0 = slice * kSlice;
     const char* row = static_cast<const char*>(P.logits) + t * P.ld * B;
 
+    const ScaleLog2 scale(scale_of(P, t));
+    const float k = scale.k, twice = scale.twice;
+
     // ------------------------------------------------ the slice, and its largest
     Raw8 x[kChunks];
     if (v0 + kSlice <= P.V) {
@@ -301,30 +304,31 @@ __global__ __launch_bounds__(kThreads, DT == MOE_DT_F32 ? 4 : 8) void k_slice(Lo
     // than an exponent holds, and z is (x - m) k, as it is for the largest scales.  Terms
     // whose z is -inf, as a masked one's is or may overflow to, have p = 0 and add nothing to
     // d: a wave that may hold one bounds z.
-    const ScaleLog2 scale(scale_of(P, t));
-    const float k = scale.k, twice = scale.twice;
     const float mk = m * k, rest = __builtin_fmaf(m, k, -mk);
     const bool far = !(fabsf(mk) < 0x1p20f) || twice != 1.f;
     const bool low = __any(!(least * k > -0x1p100f));
     float s = 0.f, d = 0.f;
-    auto sums = [&](auto plain) {
-        constexpr bool PLAIN = decltype(plain)::value;
+    auto sums = [&](auto apart, auto bounded) {
+        constexpr bool APART = decltype(apart)::value, BOUNDED = decltype(bounded)::value;
 #pragma unroll
         for (int c = 0; c < kChunks; ++c) {
             if (past(c)) continue;
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
                 const float v = elem_of<DT>(x[c], e);
-                float z = PLAIN || !far ? __builtin_fmaf(v, k, -mk) : (v - m) * k * twice;
+                float z = APART ? (v - m) * k * twice : __builtin_fmaf(v, k, -mk);
                 const float p = __builtin_amdgcn_exp2f(z);
                 s += p;
-                if constexpr (!PLAIN) z = fmaxf(z, -0x1p100f);     // 0 * -inf
+                if constexpr (BOUNDED) z = fmaxf(z, -0x1p100f);    // 0 * -inf
                 d = __builtin_fmaf(p, z, d);
             }
         }
     };
-    if (far || low) sums(std::false_type{});
-    else sums(std::true_type{});
+    const std::true_type yes;
+    const std::false_type no;
+    if (far) sums(yes, yes);
+    else if (low) sums(no, yes);
+    else sums(no, no);
     s = all_sum(s);
     d = all_sum(d);
     if (lane == 0) {
