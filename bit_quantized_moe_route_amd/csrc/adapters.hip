@@ -644,10 +644,15 @@ __global__ __launch_bounds__(256) void k_pack(moe_adapters S, int slot, const ui
 
 // The kernels for many tokens read x and the weights once for all of an adapter's ranks
 // and 32 tokens, the others once for each 16; but fewer workgroups hold less in flight.
-// Ranks 17 to 128 from T times rank tiles 8192 on (6144 -> 6144, 8 adapters, us against
-// the others: rank 64 at 1500 / 2048 / 4096 tokens 34.1 : 32.6, 48.2 : 44.1, 63.9 : 89.9;
-// rank 32 at 2048 / 4096 38.8 : 29.3, 55.3 : 63.3; rank 128 at 1024 / 2048 40.0 : 40.7,
-// 54.1 : 72.9; rank 16 at 4096 51.6 : 47.4).
+// Ranks 17 to 128 from T times rank tiles 8192 on, whatever the widths (8 adapters, us
+// against the others, for 6144 -> 6144, 6144 -> 1024, 1024 -> 6144, 256 -> 6144, 6144 -> 256):
+//   rank 32, 2800 tokens   46.0 : 44.4   23.8 : 23.3   21.7 : 25.1   20.0 : 20.7   23.1 : 21.0
+//   rank 32, 4096          55.0 : 64.8   25.9 : 31.6   36.9 : 43.0   34.9 : 37.1   23.4 : 28.4
+//   rank 64, 1500          34.0 : 36.8   27.9 : 27.3   19.2 : 21.7   17.3 : 17.2   27.3 : 25.9
+//   rank 64, 2048          38.3 : 45.8   28.2 : 31.7   22.6 : 26.2   20.9 : 20.6   27.3 : 29.2
+//   rank 128, 1024         40.1 : 43.7   31.8 : 33.3   22.7 : 25.7   19.7 : 19.2   31.5 : 31.7
+// Rank 16 stays with the others (4096 tokens, 6144 -> 6144: 51.6 : 47.4); past 128 there are
+// none for many tokens (rank 256: 258 us, against 111 of rank 128).
 bool ad_wide(const moe_adapters& S, int64_t T) {
     const int64_t rt = ad_rank_tiles(S.rank);
     return ad_plan(T, S.n).tile == 64 && rt >= 2 && rt <= kWideTiles && T * rt >= 8192;

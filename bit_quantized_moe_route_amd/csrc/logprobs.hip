@@ -16,10 +16,10 @@
 // least n and at most kCols maxima reach; those threads' logits go through LDS, where
 // the few that reach the bound are collected and ranked by counting.
 //
-// HBM bounds large batches: 2048 rows of 131072 in bf16 take 86 us without best tokens
-// (6.2 TB/s), 110 with 8 of them, since a workgroup searches when its loads are done.  A
-// row alone is two launches (5.7 and 3.1 us of kernels), 32 rows of fp32 a single wave of
-// workgroups (8.7 and 4.8).
+// HBM bounds large batches: 2048 rows of 131072 in bf16 take 84 us without best tokens
+// (6.4 TB/s), 109 with 8 of them, since a workgroup searches when its loads are done.  A
+// row alone is two launches (5.8 and 3.3 us of kernels), 32 rows of fp32 a single wave of
+// workgroups (8.6 and 5.0).
 #include "elem_dev.h"
 #include "topk_dev.h"
 
@@ -125,7 +125,7 @@ __device__ __forceinline__ float all_sum(float v) {
 }
 
 // 16-bit logits: 64 registers, so that four workgroups share a CU and some of them load
-// while the others reduce (2048 rows of 131072 bf16, 8 best tokens: 123 us against 133).
+// while the others reduce (2048 rows of 131072 bf16, 8 best tokens: 109 us against 121).
 // STREAM: logits that no cache holds.
 template <int DT, bool TOP, bool STREAM>
 __global__ __launch_bounds__(kThreads, DT == MOE_DT_F32 ? 4 : 8) void k_slice(LogArgs A) {
@@ -147,6 +147,7 @@ __global__ __launch_bounds__(kThreads, DT == MOE_DT_F32 ? 4 : 8) void k_slice(Lo
     const int v0 = slice * kSlice;
     const char* row = static_cast<const char*>(P.logits) + t * P.ld * B;
 
+    // asked for with the logits, not behind them (2048 rows: 118 -> 109 us)
     const ScaleLog2 scale(scale_of(P, t));
     const float k = scale.k, twice = scale.twice;
 
@@ -526,8 +527,8 @@ int launch_logprobs(const moe_logprobs& P, int64_t T, void* ws, void* stream) {
                 k_slice<MOE_DT_F16, TOP, STREAM><<<n * S, kThreads, 0, s>>>(A);
         };
         // More logits than the caches hold are read past them (2048 rows of 131072 bf16, no
-        // best tokens: 95.9 us against 102.4); fewer may be found there (32 rows of fp32, 20
-        // best tokens: 13.5 us against 14.4).
+        // best tokens: 84.5 us against 88.3, 8 of them: 110 against 115); fewer may be found
+        // there (32 rows of fp32, 20 best tokens: 12.5 us against 13.3).
         const bool large = T * P.V * (P.dtype == MOE_DT_F32 ? 4 : 2) >= (int64_t)1 << 28;
         auto by = [&](auto top) {
             if (large) go(top, std::true_type{});
