@@ -771,6 +771,7 @@ int moe_head_norm_rope(const moe_heads* heads, int64_t T, void* stream);
  *   logits   [device] [T, V] of dtype (F32, BF16, F16), rows ld apart, at any alignment
  *            of their elements.  -inf masks a token: p = 0, log p = -inf, and no list
  *            names it.  The type's lowest finite value is a logit like any other.
+ *            A log p below fp32's lowest value is -inf too.
  *   scale    [device] fp32 [T] (1 / temperature), or NULL: 1.
  *   ids      [device] int32 or int64 (id_bits 32, 64) [T, m], or NULL (m 0).  An id
  *            outside [0, V) gets NaN.
